@@ -86,6 +86,17 @@ def load_library():
     lib.fa_decode_paged_workspace_size.argtypes = [i, i, i, i, i]
     lib.fa_decode_paged.restype = i
     lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp, sz, vp]
+    ll = ctypes.c_longlong
+    lib.fa_kvcache_quant_page_bytes.restype = sz
+    lib.fa_kvcache_quant_page_bytes.argtypes = [i, i, i]
+    lib.fa_kvcache_append_quant.restype = i
+    lib.fa_kvcache_append_quant.argtypes = [vp, vp, ll, ll, vp, vp, vp, vp, vp] + [i] * 9 + [vp]
+    lib.fa_kvcache_read_quant.restype = i
+    lib.fa_kvcache_read_quant.argtypes = [vp] * 7 + [i] * 11 + [vp]
+    lib.fa_decode_paged_quant_workspace_size.restype = sz
+    lib.fa_decode_paged_quant_workspace_size.argtypes = [i] * 7
+    lib.fa_decode_paged_quant.restype = i
+    lib.fa_decode_paged_quant.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp, sz, vp]
     lib.fa_check_status.restype = i
     lib.fa_check_status.argtypes = [vp]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -179,6 +190,37 @@ def fa_decode_paged(q, kpages, vpages, block_table, kv_lens, o, lse, B, H, Hkv, 
                                           _ptr(o), _ptr(lse), B, H, Hkv, num_pages, page_size, max_blocks, d,
                                           float(scale), int(o_dtype), _ptr(workspace), int(workspace_bytes),
                                           _stream(stream))
+
+
+def fa_kvcache_quant_page_bytes(page_size, d, bits) -> int:
+    return int(load_library().fa_kvcache_quant_page_bytes(page_size, d, bits))
+
+
+def fa_kvcache_append_quant(k, v, stride_k, stride_v, kpages, vpages, cu_seqlens_new, block_table, kv_lens, B, Hkv,
+                            total_new, max_seqlen_new, num_pages, page_size, max_blocks, d, bits, stream=None) -> int:
+    return load_library().fa_kvcache_append_quant(_ptr(k), _ptr(v), int(stride_k), int(stride_v), _ptr(kpages),
+                                                  _ptr(vpages), _ptr(cu_seqlens_new), _ptr(block_table), _ptr(kv_lens),
+                                                  B, Hkv, total_new, max_seqlen_new, num_pages, page_size, max_blocks, d,
+                                                  bits, _stream(stream))
+
+
+def fa_kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, k_out, v_out, B, H, Hkv, total, max_seqlen,
+                          num_pages, page_size, max_blocks, d, bits, o_dtype, stream=None) -> int:
+    return load_library().fa_kvcache_read_quant(_ptr(kpages), _ptr(vpages), _ptr(cu_seqlens), _ptr(block_table),
+                                                _ptr(kv_lens), _ptr(k_out), _ptr(v_out), B, H, Hkv, total, max_seqlen,
+                                                num_pages, page_size, max_blocks, d, bits, int(o_dtype), _stream(stream))
+
+
+def fa_decode_paged_quant_workspace_size(B, H, Hkv, max_blocks, page_size, d, bits) -> int:
+    return int(load_library().fa_decode_paged_quant_workspace_size(B, H, Hkv, max_blocks, page_size, d, bits))
+
+
+def fa_decode_paged_quant(q, kpages, vpages, block_table, kv_lens, o, lse, B, H, Hkv, num_pages, page_size, max_blocks,
+                          d, bits, scale, o_dtype, workspace, workspace_bytes, stream=None) -> int:
+    return load_library().fa_decode_paged_quant(_ptr(q), _ptr(kpages), _ptr(vpages), _ptr(block_table), _ptr(kv_lens),
+                                                _ptr(o), _ptr(lse), B, H, Hkv, num_pages, page_size, max_blocks, d, bits,
+                                                float(scale), int(o_dtype), _ptr(workspace), int(workspace_bytes),
+                                                _stream(stream))
 
 
 def fa_check_status(stream=None) -> int:
@@ -342,4 +384,126 @@ def forward_blocksparse(q, k, v, block_mask, scale=None, causal=False, out_dtype
     rc = fa_forward_blocksparse(q, k, v, o, lse, m, sb, sh, B, H, Lq, Lk, d, scale, causal, _DT[out_dtype], ws,
                                 ws.numel() * ws.element_size(), stream)
     _check(rc, "fa_forward_blocksparse")
+    return o, lse
+
+
+# ----------------------------------------------------------------- quantised paged KV cache
+
+KVQ_GROUP = 32
+
+
+def _kvq_page_size(kpages, vpages, d, bits):
+    """Page size of a pair of pools, from the bytes of a page and KV head."""
+    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
+        _need(t, n, torch.uint8)
+    if kpages.dim() != 3 or kpages.shape != vpages.shape:
+        raise ValueError("kpages and vpages must both be [num_pages, Hkv, page_bytes]")
+    if d not in (64, 128, 256) or bits not in (4, 8):
+        raise FAError(FA_ERR_UNSUPPORTED, "quantised cache with d = %r, bits = %r" % (d, bits))
+    page_size, rest = divmod(kpages.shape[2], d * bits // 8 + d // KVQ_GROUP * 4)
+    if rest or page_size == 0:
+        raise ValueError("a page of %d bytes is not whole tokens of d = %d in %d bits" % (kpages.shape[2], d, bits))
+    return page_size
+
+
+def _kvq_call(first, stream, tensors):
+    """Checks that every tensor is on the first one's device.  The calls below run with that device current and, if a
+    stream is given, with it current too, so that what they allocate belongs to the stream that uses it."""
+    for t in tensors:
+        if t.device != first.device:
+            raise ValueError("all tensors must be on %s" % first.device)
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(int(stream), device=first.device)
+        return torch.cuda.stream(s)
+    return torch.cuda.device(first.device)
+
+
+def _kvq_table(block_table, kv_lens):
+    _need(block_table, "block_table", torch.int32)
+    _need(kv_lens, "kv_lens", torch.int32)
+    if block_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
+    return block_table.shape
+
+
+def kvcache_quant_pages(num_pages, Hkv, page_size, d, bits, device="cuda"):
+    """An empty (kpages, vpages) pair of pools: uint8 [num_pages, Hkv, page bytes], zeroed."""
+    n = fa_kvcache_quant_page_bytes(page_size, d, bits)
+    if n == 0:
+        raise FAError(FA_ERR_INVALID_ARG, "fa_kvcache_quant_page_bytes")
+    return tuple(torch.zeros((num_pages, Hkv, n), dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def kvcache_append_quant(k, v, kpages, vpages, cu_seqlens_new, block_table, kv_lens, max_seqlen_new, bits, stream=None):
+    """Quantises k, v [total_new, Hkv, d] (bf16; rows may be strided, as slices of a fused projection are) into the last
+    positions of each sequence: rows [cu_seqlens_new[b], cu_seqlens_new[b+1]) become positions up to kv_lens[b] (the
+    length after the append).  cu_seqlens_new int32 [B+1], block_table int32 [B,max_blocks], kv_lens int32 [B]."""
+    strides = []
+    for t, n in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+            raise ValueError("%s must be a CUDA bfloat16 tensor [total_new, Hkv, d]" % n)
+        T, Hkv, d = t.shape
+        if (d > 1 and t.stride(2) != 1) or (Hkv > 1 and t.stride(1) != d):
+            raise ValueError("the heads of a row of %s must be contiguous" % n)
+        strides.append(t.stride(0) if T > 1 else Hkv * d)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    page_size = _kvq_page_size(kpages, vpages, d, bits)
+    _need(cu_seqlens_new, "cu_seqlens_new", torch.int32)
+    B, max_blocks = _kvq_table(block_table, kv_lens)
+    if cu_seqlens_new.numel() != B + 1 or kpages.shape[1] != Hkv:
+        raise ValueError("cu_seqlens_new must be [B + 1] and the pools' KV heads k's")
+    if T == 0:
+        return
+    with _kvq_call(k, stream, (v, kpages, vpages, cu_seqlens_new, block_table, kv_lens)):
+        rc = fa_kvcache_append_quant(k, v, strides[0], strides[1], kpages, vpages, cu_seqlens_new, block_table, kv_lens, B,
+                                     Hkv, T, int(max_seqlen_new), kpages.shape[0], page_size, max_blocks, d, bits, stream)
+    _check(rc, "fa_kvcache_append_quant")
+
+
+def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, max_seqlen, H, d, bits,
+                       out_dtype=torch.bfloat16, stream=None):
+    """The last cu_seqlens[b+1] - cu_seqlens[b] rows of each sequence as k, v [total, H, d] (out_dtype), KV head
+    h / (H / Hkv) for head h: what forward_varlen takes."""
+    page_size = _kvq_page_size(kpages, vpages, d, bits)
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    B, max_blocks = _kvq_table(block_table, kv_lens)
+    if cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    num_pages, Hkv = kpages.shape[:2]
+    with _kvq_call(kpages, stream, (vpages, cu_seqlens, block_table, kv_lens)):
+        k = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
+        v = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
+        if total == 0:
+            return k, v
+        rc = fa_kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, k, v, B, H, Hkv, int(total),
+                                   int(max_seqlen), num_pages, page_size, max_blocks, d, bits, _DT[out_dtype], stream)
+    _check(rc, "fa_kvcache_read_quant")
+    return k, v
+
+
+def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None, out_dtype=torch.float32, ws=None,
+                       stream=None):
+    """decode_paged over a quantised cache: o [B,H,d] and lse [B,H] for q [B,H,d] (bf16), pools
+    [num_pages,Hkv,page bytes] (uint8), block_table int32 [B,max_blocks] and kv_lens int32 [B] (device)."""
+    _need(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, H, d]")
+    B, H, d = q.shape
+    page_size = _kvq_page_size(kpages, vpages, d, bits)
+    if _kvq_table(block_table, kv_lens)[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    num_pages, Hkv = kpages.shape[:2]
+    max_blocks = block_table.shape[1]
+    with _kvq_call(q, stream, (kpages, vpages, block_table, kv_lens) + (() if ws is None else (ws,))):
+        nbytes = fa_decode_paged_quant_workspace_size(B, H, Hkv, max_blocks, page_size, d, bits)
+        if ws is None:
+            ws = workspace(nbytes, q.device)
+        o = torch.empty((B, H, d), dtype=out_dtype, device=q.device)
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        rc = fa_decode_paged_quant(q, kpages, vpages, block_table, kv_lens, o, lse, B, H, Hkv, num_pages, page_size,
+                                   max_blocks, d, bits, 1.0 / math.sqrt(d) if scale is None else scale, _DT[out_dtype],
+                                   ws, ws.numel() * ws.element_size(), stream)
+    _check(rc, "fa_decode_paged_quant")
     return o, lse

@@ -230,6 +230,89 @@ int fa_decode_paged(const void* q, const void* kpages, const void* vpages, const
                     void* stream);
 
 /*
+ * Quantised paged KV cache: 4 or 8 bits a value, written by
+ * fa_kvcache_append_quant, read back by fa_kvcache_read_quant and attended over
+ * by fa_decode_paged_quant.  Source: "What Is FlashAttention?", "What it changes
+ * for you" (the key/value cache of a generation lives in HBM and is read once a
+ * token, so its bytes are what a decode step costs) and "The general lesson"
+ * (moving less data).  The format is not on the pages:
+ *   - The d values of a token and KV head are cut into groups of
+ *     FA_KVQ_GROUP = 32.  A group with least value lo and greatest value hi is
+ *     stored as lo (bf16, exact), s = bf16((hi - lo) / (2^bits - 1)) and the
+ *     codes c = min(rint((x - lo) * (1 / s)), 2^bits - 1); every difference,
+ *     quotient and product is one fp32 operation rounded to nearest, and rint
+ *     rounds ties to even.  It stands for lo + s c.  A step below 2^-126 is
+ *     stored as 0, its codes as 0 (the group stands for lo).  A group that holds
+ *     an infinity or NaN, or whose hi - lo overflows fp32, stands for NaN in all
+ *     its values.
+ *   - A pool is bytes [num_pages, Hkv, fa_kvcache_quant_page_bytes()]: page p
+ *     holds page_size consecutive positions of one sequence, for every KV head,
+ *     in page_size * (d * bits / 8 + d / 8) bytes (d = 128: 80 bytes a token in 4
+ *     bits, 144 in 8, against 256 in bf16).  page_size is a power of two, 16 to
+ *     65536.  K and V pools order the codes inside a page differently (csrc/
+ *     kvquant.cuh), so one is not read as the other.
+ *   - block_table int32 [B, max_blocks] and kv_lens int32 [B] as in
+ *     fa_decode_paged.  kv_lens counts the positions valid AFTER an append, so an
+ *     append, a read and a decode of one step take the same tensor.
+ * d is 64, 128 or 256, bits 4 or 8.  Pools, q, k, v and outputs must be 16-byte
+ * aligned, k and v strides multiples of 8 elements.
+ */
+#define FA_KVQ_GROUP 32
+/* Bytes of one page and KV head of a pool; 0 for invalid arguments. */
+size_t fa_kvcache_quant_page_bytes(int page_size, int d, int bits);
+
+/*
+ * Quantises new K and V rows into the cache.  k, v: bf16, token t's heads at
+ * k + t * stride_k elements, [Hkv, d] contiguous there (so they may be slices of a
+ * fused projection's rows).  cu_seqlens_new int32 [B+1] on the device: sequence b
+ * owns the rows [cu[b], cu[b+1]), at most max_seqlen_new of them, and they become
+ * its LAST positions [kv_lens[b] - n_b, kv_lens[b]).  Nothing else of the pools
+ * changes.  The positions of one call must be distinct places of the pool (two
+ * sequences that share a page may not both append to one slot of it).  On the
+ * device, a sequence whose offsets are decreasing or out of range, that has more
+ * rows than max_seqlen_new or than kv_lens[b] is skipped and flagged
+ * FA_ERR_SEQLEN; one whose length is outside [0, max_blocks * page_size] is
+ * skipped and flagged FA_ERR_KV_LEN; a row whose page is outside [0, num_pages)
+ * is not written and flagged FA_ERR_PAGE.  total_new = 0 returns FA_OK without a
+ * launch.
+ */
+int fa_kvcache_append_quant(const void* k, const void* v, long long stride_k, long long stride_v, void* kpages,
+                            void* vpages, const int* cu_seqlens_new, const int* block_table, const int* kv_lens, int B,
+                            int Hkv, int total_new, int max_seqlen_new, int num_pages, int page_size, int max_blocks,
+                            int d, int bits, void* stream);
+
+/*
+ * Reads the last rows of each sequence back: row cu_seqlens[b] + i of k_out and
+ * v_out [total, H, d] (o_dtype) is position kv_lens[b] - n_b + i, n_b =
+ * cu_seqlens[b+1] - cu_seqlens[b] <= max_seqlen (n_b = kv_lens[b] reads all of
+ * it).  Head h of the output is KV head h / (H / Hkv): with H query heads the
+ * result is what fa_forward_varlen takes as k and v (a prefill over a cached
+ * prefix); with H = Hkv it is the cache.  A value is lo + s c rounded to fp32, then
+ * to o_dtype.  Invalid sequences are skipped and flagged as by
+ * fa_kvcache_append_quant (their rows are not written); a page outside
+ * [0, num_pages) is flagged FA_ERR_PAGE and read as page 0.  Rows at or past
+ * cu_seqlens[B] are not written.
+ */
+int fa_kvcache_read_quant(const void* kpages, const void* vpages, const int* cu_seqlens, const int* block_table,
+                          const int* kv_lens, void* k_out, void* v_out, int B, int H, int Hkv, int total, int max_seqlen,
+                          int num_pages, int page_size, int max_blocks, int d, int bits, int o_dtype, void* stream);
+
+/* Workspace bytes fa_decode_paged_quant needs; 0 for invalid arguments. */
+size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits);
+
+/*
+ * fa_decode_paged over a quantised cache: the exact softmax attention of q
+ * [B, H, d] (bf16) over the values that the first kv_lens[b] positions stand for.
+ * o [B, H, d] (o_dtype), lse [B, H] fp32, and the device-side conditions
+ * (FA_ERR_KV_LEN, FA_ERR_PAGE, a length of 0) are those of fa_decode_paged.
+ * What a page holds past a sequence's length never changes a result.
+ */
+int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
+                          const int* kv_lens, void* o, float* lse, int B, int H, int Hkv, int num_pages, int page_size,
+                          int max_blocks, int d, int bits, float scale, int o_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
  * Forward pass under a block-sparse mask.  The glossary entry's "Common
  * misconceptions" names a block-sparse extension that changes which query/key
  * pairs attend, as distinct from the dense exact calculation; the pages give no
