@@ -1,26 +1,57 @@
 // Single-query decode over the quantised paged cache: fa_decode_paged_quant
 // (declared in include/fa.h, cache format in kvquant.cuh).
 //
-// With K and V held as lo + s c per group of 32 dimensions, a score is
+// Mathematics.  With K and V held as lo + s c per group of 32 dimensions,
 //     q . k_j = sum_g [ s_jg (q_g . c_jg) + lo_jg sum(q_g) ]
-// and the output follows the online softmax of fa_decode: running max, running
-// sum, unnormalised accumulator, split over the keys and merged by log-sum-exp.
-//   fa_decode_quant_split    a CTA per (b, h, split): every kMaxSplits-th tile of 128 keys
-//   fa_decode_quant_combine  a CTA per (b, h): merges the splits
+//     o_d     = sum_j p_j lo_jg + sum_j (p_j s_jg) c_jd          (g = d / 32)
+// so the codes go into the matrix instructions as they are and a group's lo and s
+// are applied to its 16x8 partial sums (scores) or to the probabilities (output).
+// The rest is the online softmax of fa_decode, in base 2.
+//
+// Codes as fp16.  A code c in the low bits of a half is the fp16 subnormal c 2^-24,
+// exactly: an AND with 0x000f000f (0x00ff00ff) of a 32-bit word gives two of them,
+// no conversion.  With 0x00f000f0 it gives 16 c 2^-24, and the 1/16 goes into the
+// other operand (scores) or the result (output).  q is scaled by a power of two per
+// head so that its largest value is in [2^14, 2^15): fp16 then holds every bf16 of
+// it exactly down to 2^-29 of that, and to 2^-40 in absolute terms.  The weights
+// p s are rounded to fp16 (11 bits; bf16 has 8) and are below 2^14 by choice of the
+// running reference, so that full precision reaches down to 2^-28 of the greatest.
+//
+// mma.sync m16n8k16 with the keys (scores) or dimensions (output) as the 16 rows and
+// the heads that share the KV head as the 8 columns: NT = 1 or 2 tiles of 8.  Scores
+// come out as [key][head] and go through shared memory once, where each thread picks
+// up 4 keys of a head: the layout the weights need as the second product's B operand.
+// A fragments are one 16-byte (K) or 8-byte (V) shared-memory load a key and plane,
+// which is what the cache's order of dimensions inside a token is for.
+//
+// Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  The units
+// of the whole batch, in that order, are cut into equal runs, one a CTA; warp w of a
+// CTA takes every eighth unit of its run.  Each warp copies its own units into a ring of S
+// stages with 1-D bulk copies (a 16-token tile of K or of V is one run of bytes), so
+// nothing in the loop waits for another warp.  Where the run crosses into another
+// (sequence, head set), the eight warps merge their statistics and write the output,
+// or, if the set's keys are shared with another CTA, a partial one that
+// fa_decode_quant_combine merges.  Every wait is bounded.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 #include "fa_internal.h"
 #include "kvquant.cuh"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kSplitKeys = 128;  // keys of a tile, threads of a CTA
-constexpr int kMaxSplits = 64;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxCtas = 2 * 160;   // CTAs of a launch (bounds the workspace)
+constexpr int kMergeDims = 64;      // dimensions merged at once
+constexpr float kRefBits = 6.0f;    // weights are 2^kRefBits times p s / 2^E at the running maximum
+constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 
 struct DecodeQuantParams {
     const __nv_bfloat16* q;  // [B, H, D]
@@ -31,144 +62,694 @@ struct DecodeQuantParams {
     void* o;
     float* lse;
     int* status;
-    float* part_o;    // [B * H, splits, D], normalised
-    float* part_lse;  // [B * H, splits]
-    int B, H, Hkv, num_pages, page_shift, max_blocks, splits, cap;
-    float scale;
+    float* part_o;    // [2 * CTAs][8 NT][D], normalised
+    float* part_lse;  // [2 * CTAs][8 NT], base 2
+    int4* first;      // [CTAs]: (sequence, head set, first unit, units) of the set that holds a CTA's first unit
+    int2* plan;       // units of the batch, CTAs that share them
+    int B, H, Hkv, num_pages, page_shift, max_blocks, cap, sets;  // sets: head sets of a KV head
+    float scale, scale_log2;
     int o_dtype;
 };
 
-template <int D, int BITS, int U>
-__device__ __forceinline__ uint32_t code_at(const uint8_t* tile, int r, int dim) {
+#ifdef FA_TEST_HOOKS
+// One-shot fault (test build only): the next stage a warp would fill gets neither its
+// expected byte count nor its copies, so the warp's wait for it runs out.
+__device__ int g_test_skip_quant;
+#endif
+
+template <int D, int BITS, int NT>
+struct Cfg {
     using F = KvqFormat<D, BITS>;
-    const int plane = dim / F::kPlaneDims, i = dim % F::kPlaneDims;
-    const int g = i / kKvqGroup, u = (i % kKvqGroup) / U, j = i % U;
-    const int bit = (u * F::kPlaneGroups + g) * U * BITS + j * BITS;
-    const uint32_t byte = tile[plane * kKvqTile * F::kPlaneBytes + r * F::kPlaneBytes + bit / 8];
-    return (byte >> (bit % 8)) & ((1u << BITS) - 1u);
+    // two CTAs an SM need 128 registers a thread: O alone is NT D / 4 of them
+    static constexpr int kCtas = NT * D <= 128 ? 2 : 1;
+    static constexpr int kStageBudget = kCtas == 2 ? 10400 : 20800;  // bytes of a warp's ring
+    static constexpr int kBlocks = 8 * F::kTileBytes <= kStageBudget ? 2 : 1;  // tiles of a unit
+    static constexpr int KT = 16 * kBlocks;
+    static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
+    static constexpr int kStageBytes = 2 * kHalf;
+    static constexpr int S = kStageBudget / kStageBytes < 4 ? kStageBudget / kStageBytes : 4;
+    static constexpr int HP = 8 * NT;  // heads of a set
+    static constexpr int kScoreStride = KT + 4;
+    // shared memory
+    static constexpr int kRedBytes = HP * kMergeDims * 4;  // of a warp; its score tile is kept there too
+    static constexpr int kRingOff = 0;
+    static constexpr int kRedOff = kRingOff + kWarps * S * kStageBytes;
+    static constexpr int kZOff = kRedOff + kWarps * kRedBytes;           // [warp][head][group]
+    static constexpr int kMOff = kZOff + kWarps * HP * F::kGroups * 4;   // [warp][head] reference
+    static constexpr int kLOff = kMOff + kWarps * HP * 4;                // [warp][head] sum
+    static constexpr int kBarOff = kLOff + kWarps * HP * 4;
+    static constexpr int kMiscOff = kBarOff + kWarps * S * 8;
+    static constexpr int kBytes = kMiscOff + 64 + 128;
+    static_assert(S >= 2, "a stage is copied while another is read");
+    static_assert(HP * kScoreStride * 4 <= kRedBytes, "a warp's scores fit its merge buffer");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// fp16 pair, lo in bits 0-15
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t param) { return __uint_as_float(param << 16); }
+__device__ __forceinline__ float s_of(uint32_t param) { return __uint_as_float(param & 0xFFFF0000u); }
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&r)[N], const uint8_t* p) {
+    if constexpr (N == 1) {
+        r[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r[0] = v.x, r[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+        }
+    }
 }
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kSplitKeys) fa_decode_quant_split(const DecodeQuantParams p) {
-    using F = KvqFormat<D, BITS>;
-    __shared__ float s_q[D], s_qsum[F::kGroups], s_p[kSplitKeys], s_red[kSplitKeys / 32];
-    __shared__ const uint8_t* s_v[kSplitKeys];
-    if (*p.status == FA_ERR_TIMEOUT) return;
-    const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, hkv = h / (p.H / p.Hkv);
-    const int tid = threadIdx.x;
-    int len = p.kv_lens[b];
-    if (len < 0 || len > p.cap) {
-        if (tid == 0) atomicCAS(p.status, 0, FA_ERR_KV_LEN);
-        len = len < 0 ? 0 : p.cap;
+template <int KT>
+__device__ __forceinline__ int units_of(int len) {
+    return static_cast<int>((static_cast<unsigned>(len) + KT - 1) / KT);
+}
+__device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
+
+// A place in the batch's order of units: the set that unit v belongs to.
+template <int KT>
+struct Cursor {
+    int b, hh, begin, n, len;  // sequence, set (KV head and head set), first unit, units, keys
+    __device__ __forceinline__ void seek(const DecodeQuantParams& p, int v) {
+        while (v >= begin + n) {
+            begin += n;
+            if (++hh == p.Hkv * p.sets) {
+                hh = 0;
+                do {
+                    ++b;
+                    len = clamp_len(p.kv_lens[b], p.cap);
+                } while (len == 0);
+                n = units_of<KT>(len);
+            }
+        }
     }
-    for (int i = tid; i < D; i += kSplitKeys) s_q[i] = __bfloat162float(p.q[static_cast<size_t>(bh) * D + i]);
+};
+
+template <int D, int BITS, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
+    using C = Cfg<D, BITS, NT>;
+    using F = KvqFormat<D, BITS>;
+    constexpr int KT = C::KT, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float* red_all = reinterpret_cast<float*>(smem + C::kRedOff);
+    float* red_z = reinterpret_cast<float*>(smem + C::kZOff);
+    float* red_m = reinterpret_cast<float*>(smem + C::kMOff);
+    float* red_l = reinterpret_cast<float*>(smem + C::kLOff);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * S;
+    int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] abort, [1..4] first set, [8..15] scan
+    volatile int* abort_flag = misc;
+
+    // ---- plan: the number of units and the set of this CTA's first one
+    if (tid == 0) *abort_flag = (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) ? 1 : 0;
+    if (lane == 0) {
+        for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    const int HH = p.Hkv * p.sets;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int len = p.kv_lens[b];
+        if (blockIdx.x == 0 && (len < 0 || len > p.cap)) atomicCAS(p.status, 0, FA_ERR_KV_LEN);
+        mine += units_of<KT>(clamp_len(len, p.cap));
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    if (lane == 31) misc[8 + warp] = incl;
     __syncthreads();
-    if (tid < F::kGroups) {
-        float a = 0.0f;
-        for (int i = 0; i < kKvqGroup; ++i) a += s_q[tid * kKvqGroup + i];
-        s_qsum[tid] = a;
+    if (*abort_flag) return;
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) incl += total;
+        total += misc[8 + i];
     }
+    const int U = total * HH;
+    // a CTA has a unit for each of its warps before another one is used
+    const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / kWarps));
+    const int cta = blockIdx.x;
+    if (cta == 0 && tid == 0) *p.plan = make_int2(U, n_cta);
+    if (cta >= n_cta) return;
+    // sequences without keys
+    for (int b = cta; b < p.B; b += n_cta) {
+        if (p.kv_lens[b] > 0) continue;
+        for (int i = tid; i < p.H * D; i += kThreads) {
+            const size_t at = static_cast<size_t>(b) * p.H * D + i;
+            if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[at] = 0.0f;
+            else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(0.0f);
+        }
+        for (int i = tid; i < p.H; i += kThreads) p.lse[static_cast<size_t>(b) * p.H + i] = -INFINITY;
+    }
+    if (U == 0) return;
+    const int u0 = static_cast<int>(static_cast<long long>(U) * cta / n_cta);
+    const int u1 = static_cast<int>(static_cast<long long>(U) * (cta + 1) / n_cta);
+    {
+        // the thread whose sequences hold unit u0
+        const int lo = (incl - mine) * HH, hi = incl * HH;
+        if (u0 >= lo && u0 < hi) {
+            int at = lo;
+            for (int b = b0; b < b1; ++b) {
+                const int len = clamp_len(p.kv_lens[b], p.cap), n = units_of<KT>(len);
+                if (u0 < at + n * HH) {
+                    const int hh = (u0 - at) / n;
+                    misc[1] = b, misc[2] = hh, misc[3] = at + hh * n, misc[4] = len;
+                    p.first[cta] = make_int4(b, hh, at + hh * n, n);
+                    break;
+                }
+                at += n * HH;
+            }
+        }
+    }
+    __syncthreads();
+    Cursor<KT> cur{misc[1], misc[2], misc[3], units_of<KT>(misc[4]), misc[4]};
+    Cursor<KT> ahead = cur;
+    const int group = p.H / p.Hkv;
+
+    // ---- copies: this warp's units u0 + warp + 8 i, stage i % S
+    uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    float m = -INFINITY, l = 0.0f, acc[(D + kSplitKeys - 1) / kSplitKeys] = {};
-    for (int k0 = blockIdx.y * kSplitKeys; k0 < len; k0 += gridDim.y * kSplitKeys) {
-        __syncthreads();
-        const int key = k0 + tid;
-        float x = -INFINITY;
-        if (key < len) {
-            int pg = p.block_table[static_cast<size_t>(b) * p.max_blocks + (key >> p.page_shift)];
-            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.num_pages)) {
+    int v_load = u0 + warp;  // next unit to copy
+    int n_load = 0;          // units copied
+    int skipped = -1;
+    int page = -1, left = 0;  // of unit v_load: lane i's page and the unit's valid keys
+    auto look_up = [&]() {
+        if (v_load >= u1) return;
+        ahead.seek(p, v_load);
+        const int key0 = (v_load - ahead.begin) * KT;
+        left = min(KT, ahead.len - key0);
+        if (lane < NB && lane * 16 < left) {
+            page = p.block_table[static_cast<size_t>(ahead.b) * p.max_blocks + ((key0 + lane * 16) >> p.page_shift)];
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
                 atomicCAS(p.status, 0, FA_ERR_PAGE);
-                pg = 0;
+                page = 0;
             }
-            const int slot = key & ((1 << p.page_shift) - 1), r = slot % kKvqTile;
-            const size_t off = (static_cast<size_t>(pg) * p.Hkv + hkv) * block_bytes +
-                               static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
-            const uint8_t* kt = p.kpages + off;
-            s_v[tid] = p.vpages + off;
-            x = 0.0f;
-            for (int g = 0; g < F::kGroups; ++g) {
-                float dot = 0.0f;
-                for (int i = 0; i < kKvqGroup; ++i)
-                    dot = fmaf(s_q[g * kKvqGroup + i],
-                               static_cast<float>(code_at<D, BITS, kKvqUnitK>(kt, r, g * kKvqGroup + i)), dot);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(kt + F::kParamOff + r * F::kParamBytes + g * 4);
-                x = fmaf(__uint_as_float(w & 0xFFFF0000u), dot, fmaf(__uint_as_float(w << 16), s_qsum[g], x));
-            }
-            x *= p.scale;
         }
-        float mx = x;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (tid % 32 == 0) s_red[tid / 32] = mx;
-        __syncthreads();
-        float m_new = m;
-        for (int i = 0; i < kSplitKeys / 32; ++i) m_new = fmaxf(m_new, s_red[i]);
-        const float mb = m_new == -INFINITY ? 0.0f : m_new;
-        const float alpha = m == -INFINITY ? 0.0f : expf(m - mb);
-        s_p[tid] = expf(x - mb);
-        __syncthreads();
-        l *= alpha;
-        m = m_new;
-        const int n = min(kSplitKeys, len - k0);
-        for (int j = 0; j < n; ++j) l += s_p[j];
+    };
+    auto issue = [&]() {
+        if (v_load >= u1) return;
+        const int s = n_load % S;
+        bool skip = false;
+#ifdef FA_TEST_HOOKS
+        int armed = 0;
+        if (lane == 0) armed = atomicExch(&g_test_skip_quant, 0);
+        skip = __shfl_sync(0xffffffffu, armed, 0) != 0;
+        if (skip) skipped = n_load;
+#endif
+        if (!skip) {
+            const int nb = (left + 15) / 16;
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb) * 2 * F::kTileBytes);
+            __syncwarp();
+            if (lane < nb) {
+                const int slot = ((v_load - ahead.begin) * KT + lane * 16) & ((1 << p.page_shift) - 1);
+                const size_t off = (static_cast<size_t>(page) * p.Hkv + ahead.hh / p.sets) * block_bytes +
+                                   static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
+                uint8_t* dst = ring + s * C::kStageBytes + lane * F::kTileBytes;
+                bulk_load(dst, p.kpages + off, F::kTileBytes, &full[s]);
+                bulk_load(dst + C::kHalf, p.vpages + off, F::kTileBytes, &full[s]);
+            }
+            __syncwarp();
+        }
+        ++n_load;
+        v_load += kWarps;
+        look_up();
+    };
+    look_up();
+    for (int i = 0; i < S - 1; ++i) issue();
+
+    // ---- the sets of this CTA's run
+    const int r = lane >> 2, t = lane & 3;
+    float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
+    int v = u0 + warp, n_done = 0;
+    bool ok = true;
+    for (int at = u0; at < u1;) {
+        cur.seek(p, at);
+        const int end = min(u1, cur.begin + cur.n);
+        const int hkv = cur.hh / p.sets, h_in = (cur.hh - hkv * p.sets) * HP;
+        const int G = min(HP, group - h_in);  // heads of the set
+        const size_t head0 = static_cast<size_t>(cur.b) * p.H + hkv * group + h_in;
+
+        float o[NT][D / 16][4];
+        float oz[NT][NG], m[NT], l[NT];
+        int E = -1000;
+        // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
+        uint32_t qb[NT][NG][4];
+        float qs[NT][NG][2], A[NT][2];  // of the score fragment's heads 2 t, 2 t + 1
 #pragma unroll
-        for (int e = 0; e < (D + kSplitKeys - 1) / kSplitKeys; ++e) {
-            const int dim = e * kSplitKeys + tid;
-            if (dim >= D) break;
-            float a = acc[e] * alpha;
-            for (int j = 0; j < n; ++j) {
-                const int r = ((k0 + j) & ((1 << p.page_shift) - 1)) % kKvqTile;
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(s_v[j] + F::kParamOff + r * F::kParamBytes +
-                                                                      dim / kKvqGroup * 4);
-                const float c = static_cast<float>(code_at<D, BITS, kKvqUnitV>(s_v[j], r, dim));
-                a = fmaf(s_p[j], fmaf(__uint_as_float(w & 0xFFFF0000u), c, __uint_as_float(w << 16)), a);
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = -INFINITY;
+            l[nt] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
+            uint4 raw[NG];
+            const int h = nt * 8 + r;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                oz[nt][g] = 0.0f;
+                raw[g] = h < G ? *reinterpret_cast<const uint4*>(p.q + (head0 + h) * D + g * kKvqGroup + t * 8)
+                               : make_uint4(0, 0, 0, 0);
             }
-            acc[e] = a;
+            uint32_t big = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = (&raw[g].x)[i];
+                    big = max(big, max((w << 16) & 0x7FFFFFFFu, w & 0x7FFF0000u));
+                }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int e = max(static_cast<int>(big >> 23) - 127, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
+            const float a_own = ldexpf(p.scale_log2, 10 + e);                             // undoes it and the codes' 2^-24
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float f[8], sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = (&raw[g].x)[i];
+                    f[2 * i] = bf16lo_to_f32(w);
+                    f[2 * i + 1] = bf16hi_to_f32(w);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sum += f[i];
+                    f[i] *= up;
+                }
+                if constexpr (BITS == 4) {
+                    qb[nt][g][0] = pack_f16x2(f[0], f[4]);
+                    qb[nt][g][1] = pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f);
+                    qb[nt][g][2] = pack_f16x2(f[2], f[6]);
+                    qb[nt][g][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
+                } else {
+                    qb[nt][g][0] = pack_f16x2(f[0], f[2]);
+                    qb[nt][g][1] = pack_f16x2(f[1], f[3]);
+                    qb[nt][g][2] = pack_f16x2(f[4], f[6]);
+                    qb[nt][g][3] = pack_f16x2(f[5], f[7]);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum *= p.scale_log2;
+                qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
+                qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+            }
+            A[nt][0] = __shfl_sync(0xffffffffu, a_own, 8 * t);
+            A[nt][1] = __shfl_sync(0xffffffffu, a_own, 8 * t + 4);
         }
+
+        for (; v < end; v += kWarps, ++n_done) {
+            if (ok) issue();
+            const int s = n_done % S;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (n_done / S) & 1, abort_flag, p.status));
+            if (!ok) continue;
+            uint8_t* ks = ring + s * C::kStageBytes;
+            uint8_t* vs = ks + C::kHalf;
+            const int valid = min(KT, cur.len - (v - cur.begin) * KT);
+            const int nb = (valid + 15) / 16;
+            if (valid < KT) {
+                // Slots past the last key may hold anything: their V parameters become zero
+                // (a zero probability would not cancel a NaN), their scores -inf below.
+                for (int i = lane; i < KT * NG; i += 32) {
+                    const int key = i / NG;
+                    if (key >= valid)
+                        *reinterpret_cast<uint32_t*>(vs + (key / 16) * F::kTileBytes + F::kParamOff +
+                                                     (key % 16) * F::kParamBytes + (i % NG) * 4) = 0u;
+                }
+                __syncwarp();
+                fence_proxy_async_smem();  // before the stage's next bulk copy
+            }
+            // ---- scores
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                if (kb >= nb) break;
+                const uint8_t* kt = ks + kb * F::kTileBytes;
+                uint32_t par0[NG], par1[NG];  // keys r and r + 8
+                lds_words(par0, kt + F::kParamOff + r * F::kParamBytes);
+                lds_words(par1, kt + F::kParamOff + (r + 8) * F::kParamBytes);
+                float x1[NT][4], x2[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x1[nt][i] = x2[nt][i] = 0.0f;
+#pragma unroll
+                for (int pl = 0; pl < F::kPlanes; ++pl) {
+                    constexpr int W = F::kPlaneBytes / 16;  // words of a thread and row
+                    uint32_t c0[W], c1[W];
+                    lds_words(c0, kt + (pl * 16 + r) * F::kPlaneBytes + t * (F::kPlaneBytes / 4));
+                    lds_words(c1, kt + (pl * 16 + r + 8) * F::kPlaneBytes + t * (F::kPlaneBytes / 4));
+#pragma unroll
+                    for (int gp = 0; gp < PG; ++gp) {
+                        const int g = pl * PG + gp;
+                        float acc[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t a0, a1, a2, a3;
+                            if constexpr (BITS == 4) {
+                                const uint32_t w0 = c0[gp] >> (8 * st), w1 = c1[gp] >> (8 * st);
+                                a0 = w0 & 0x000F000Fu, a1 = w1 & 0x000F000Fu;
+                                a2 = w0 & 0x00F000F0u, a3 = w1 & 0x00F000F0u;
+                            } else {
+                                const uint32_t w0 = c0[2 * gp + st], w1 = c1[2 * gp + st];
+                                a0 = w0 & 0x00FF00FFu, a1 = w1 & 0x00FF00FFu;
+                                a2 = (w0 >> 8) & 0x00FF00FFu, a3 = (w1 >> 8) & 0x00FF00FFu;
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * st], qb[nt][g][2 * st + 1]);
+                        }
+                        const float s0 = s_of(par0[g]), s1 = s_of(par1[g]), z0 = lo_of(par0[g]), z1 = lo_of(par1[g]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            x1[nt][0] = fmaf(s0, acc[nt][0], x1[nt][0]);
+                            x1[nt][1] = fmaf(s0, acc[nt][1], x1[nt][1]);
+                            x1[nt][2] = fmaf(s1, acc[nt][2], x1[nt][2]);
+                            x1[nt][3] = fmaf(s1, acc[nt][3], x1[nt][3]);
+                            x2[nt][0] = fmaf(z0, qs[nt][g][0], x2[nt][0]);
+                            x2[nt][1] = fmaf(z0, qs[nt][g][1], x2[nt][1]);
+                            x2[nt][2] = fmaf(z1, qs[nt][g][0], x2[nt][2]);
+                            x2[nt][3] = fmaf(z1, qs[nt][g][1], x2[nt][3]);
+                        }
+                    }
+                }
+                // key j of the block is kept in column 4 (j % 4) + j / 4
+                const int col = kb * 16 + 4 * (r & 3) + (r >> 2);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float* row = sc + (nt * 8 + 2 * t) * C::kScoreStride + col;
+                    row[0] = fmaf(x1[nt][0], A[nt][0], x2[nt][0]);
+                    row[C::kScoreStride] = fmaf(x1[nt][1], A[nt][1], x2[nt][1]);
+                    row[2] = fmaf(x1[nt][2], A[nt][0], x2[nt][2]);
+                    row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
+                }
+            }
+            // E: every step of the unit's V is below 2^E
+            uint32_t top = 0;
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                if (kb >= nb) break;
+                uint32_t w[NG / 2];
+                lds_words(w, vs + kb * F::kTileBytes + F::kParamOff + lane * (NG / 2 * 4));
+#pragma unroll
+                for (int i = 0; i < NG / 2; ++i) top = max(top, w[i]);
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e_unit = min(max(static_cast<int>(top >> 23) - 126, -100), 120);
+            __syncwarp();
+            // ---- softmax: thread (head r, t) takes keys t, t + 4, t + 8, t + 12 of each block
+            float u[NT][4 * NB];
+            bool grow = e_unit > E;
+            float m_new[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) {
+                    const float4 x = *reinterpret_cast<const float4*>(sc + (nt * 8 + r) * C::kScoreStride + kb * 16 + 4 * t);
+                    u[nt][4 * kb] = x.x, u[nt][4 * kb + 1] = x.y, u[nt][4 * kb + 2] = x.z, u[nt][4 * kb + 3] = x.w;
+                }
+                if (valid < KT) {
+#pragma unroll
+                    for (int i = 0; i < 4 * NB; ++i)
+                        if ((i >> 2) * 16 + (i & 3) * 4 + t >= valid) u[nt][i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) mx = fmaxf(mx, u[nt][i]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                m_new[nt] = fmaxf(m[nt], mx);
+                grow |= m[nt] == -INFINITY ? m_new[nt] != -INFINITY : m_new[nt] - m[nt] > kGrowBits;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                const int e_new = max(E, e_unit);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float alpha = m[nt] == -INFINITY ? 0.0f : ex2_approx((m[nt] - m_new[nt]) + static_cast<float>(E - e_new));
+                    m[nt] = m_new[nt];
+                    l[nt] *= alpha;
+                    const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) oz[nt][g] *= alpha;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[nt][j][0] *= al0;
+                        o[nt][j][1] *= al1;
+                        o[nt][j][2] *= al0;
+                        o[nt][j][3] *= al1;
+                    }
+                }
+                E = e_new;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float bias = kRefBits - static_cast<float>(E) - (m[nt] == -INFINITY ? 0.0f : m[nt]);
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) {
+                    u[nt][i] = ex2_approx(u[nt][i] + bias);
+                    l[nt] += u[nt][i];
+                }
+            }
+            // ---- output
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                if (kb >= nb) break;
+                const uint8_t* vt = vs + kb * F::kTileBytes;
+                uint32_t wb[NT][NG][2];  // p s of keys (t, t + 4) and (t + 8, t + 12)
+                {
+                    uint32_t par[4][NG];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lds_words(par[i], vt + F::kParamOff + (4 * i + t) * F::kParamBytes);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float* uu = u[nt] + 4 * kb;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            wb[nt][g][0] = pack_f16x2(uu[0] * s_of(par[0][g]), uu[1] * s_of(par[1][g]));
+                            wb[nt][g][1] = pack_f16x2(uu[2] * s_of(par[2][g]), uu[3] * s_of(par[3][g]));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) oz[nt][g] = fmaf(uu[i], lo_of(par[i][g]), oz[nt][g]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int pl = 0; pl < F::kPlanes; ++pl) {
+                    constexpr int W = F::kPlaneBytes / 32;
+                    uint32_t c[4][W];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        lds_words(c[i], vt + (pl * 16 + 4 * i + t) * F::kPlaneBytes + r * (F::kPlaneBytes / 8));
+#pragma unroll
+                    for (int gp = 0; gp < PG; ++gp) {
+                        const int g = pl * PG + gp;
+                        // per 32-bit word: 2 groups of 4 nibbles, or 1 group of 4 bytes
+                        const int w = BITS == 4 ? gp / 2 : gp;
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            uint32_t a0, a1, a2, a3;
+                            if constexpr (BITS == 4) {
+                                const int sel = gp % 2 ? 0x7632 : 0x5410;
+                                const uint32_t x = __byte_perm(c[0][w], c[1][w], sel) >> (8 * st);
+                                const uint32_t y = __byte_perm(c[2][w], c[3][w], sel) >> (8 * st);
+                                a0 = x & 0x000F000Fu, a1 = x & 0x00F000F0u;
+                                a2 = y & 0x000F000Fu, a3 = y & 0x00F000F0u;
+                            } else {
+                                const int sel = st ? 0x7632 : 0x5410;
+                                const uint32_t x = __byte_perm(c[0][w], c[1][w], sel);
+                                const uint32_t y = __byte_perm(c[2][w], c[3][w], sel);
+                                a0 = x & 0x00FF00FFu, a1 = (x >> 8) & 0x00FF00FFu;
+                                a2 = y & 0x00FF00FFu, a3 = (y >> 8) & 0x00FF00FFu;
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(o[nt][2 * g + st], a0, a1, a2, a3, wb[nt][g][0], wb[nt][g][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage and the scores may be overwritten
+        }
+
+        // ---- merge the eight warps: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of heads 2 t, 2 t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+            const int at_h = warp * HP + nt * 8 + r;
+            if (t == 0) {
+                red_m[at_h] = m[nt] == -INFINITY ? -INFINITY : m[nt] + static_cast<float>(E);
+                red_l[at_h] = l[nt];
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                oz[nt][g] += __shfl_xor_sync(0xffffffffu, oz[nt][g], 1);
+                oz[nt][g] += __shfl_xor_sync(0xffffffffu, oz[nt][g], 2);
+                if (t == 0) red_z[at_h * NG + g] = oz[nt][g];
+            }
+        }
+        const bool whole = at == cur.begin && end == cur.begin + cur.n;
+        const int slot = 2 * cta + (at > cur.begin ? 0 : 1);
+        constexpr float kUp = 16777216.0f;  // 2^24 of the codes
+        constexpr float kUp1 = BITS == 4 ? kUp / 16.0f : kUp;
+#pragma unroll
+        for (int md = 0; md < D / kMergeDims; ++md) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int gi = 0; gi < kMergeDims / kKvqGroup; ++gi) {
+                    const int g = md * (kMergeDims / kKvqGroup) + gi;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float* o0 = o[nt][2 * g];
+                        const float* o1 = o[nt][2 * g + 1];
+                        *reinterpret_cast<float4*>(sc + (nt * 8 + 2 * t + c) * kMergeDims + gi * kKvqGroup + 4 * r) =
+                            make_float4(o0[c] * kUp, o0[c + 2] * kUp1, o1[c] * kUp, o1[c + 2] * kUp1);
+                    }
+                }
+            __syncthreads();
+            const bool aborted = *abort_flag != 0;
+            for (int e = tid; !aborted && e < G * kMergeDims; e += kThreads) {
+                const int h = e / kMergeDims, c = e % kMergeDims, d = md * kMergeDims + c;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_m[w * HP + h]);
+                float L = 0.0f, O = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float mw = red_m[w * HP + h];
+                    // no finite score: nothing seen, or only NaN and -inf (then l and O say so)
+                    const float wt = mw == M ? 1.0f : ex2_approx(mw - M);
+                    L = fmaf(wt, red_l[w * HP + h], L);
+                    O = fmaf(wt, red_all[(w * HP + h) * kMergeDims + c] + red_z[(w * HP + h) * NG + d / kKvqGroup], O);
+                }
+                O /= L;
+                if (whole) {
+                    if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[(head0 + h) * D + d] = O;
+                    else static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(O);
+                    if (d == 0) p.lse[head0 + h] = (M - kRefBits + log2f(L)) * 0.6931471805599453f;
+                } else {
+                    p.part_o[(static_cast<size_t>(slot) * HP + h) * D + d] = O;
+                    if (d == 0) p.part_lse[slot * HP + h] = M - kRefBits + log2f(L);
+                }
+            }
+            __syncthreads();
+        }
+        at = end;
     }
-    const size_t part = static_cast<size_t>(bh) * p.splits + blockIdx.y;
-#pragma unroll
-    for (int e = 0; e < (D + kSplitKeys - 1) / kSplitKeys; ++e)
-        if (e * kSplitKeys + tid < D) p.part_o[part * D + e * kSplitKeys + tid] = l > 0.0f || l != l ? acc[e] / l : 0.0f;
-    if (tid == 0) p.part_lse[part] = m == -INFINITY && l == 0.0f ? -INFINITY : m + logf(l);
+    // after a wait that ran out: every copy issued here lands before the shared memory goes away
+    for (int i = n_done > 0 && !ok ? max(0, n_load - S) : n_load; i < n_load; ++i)
+        if (i != skipped) mbar_wait_drain(&full[i % S], (i / S) & 1, p.status);
 }
 
-template <int D>
-__global__ void __launch_bounds__(D) fa_decode_quant_combine(const DecodeQuantParams p) {
-    if (*p.status == FA_ERR_TIMEOUT) return;
-    const size_t bh = blockIdx.x;
-    const float* lse = p.part_lse + bh * p.splits;
-    float M = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) M = fmaxf(M, lse[s]);
-    float L = 0.0f, O = 0.0f;
-    for (int s = 0; s < p.splits; ++s) {
-        if (lse[s] == -INFINITY) continue;
-        const float w = expf(lse[s] - M);
-        L += w;
-        O = fmaf(w, p.part_o[(bh * p.splits + s) * D + threadIdx.x], O);
+// CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
+// CTAs has P - 1 such blocks, each of which merges a share of its outputs.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
+    constexpr int HP = 8 * NT;
+    if (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) return;
+    const int2 plan = *p.plan;
+    const int i = blockIdx.x + 1;
+    if (i >= plan.y) return;
+    const long long U = plan.x, n_cta = plan.y;
+    const int4 set = p.first[i];  // sequence, set, first unit, units
+    if (set.z == static_cast<int>(U * i / n_cta)) return;  // starts with the CTA
+    const int c0 = static_cast<int>(((set.z + 1LL) * n_cta - 1) / U);
+    const int c1 = static_cast<int>((static_cast<long long>(set.z + set.w) * n_cta - 1) / U);
+    const int hkv = set.y / p.sets, group = p.H / p.Hkv, h_in = (set.y - hkv * p.sets) * HP;
+    const int G = min(HP, group - h_in);
+    const size_t head0 = static_cast<size_t>(set.x) * p.H + hkv * group + h_in;
+    const int share = (G * D + c1 - c0 - 1) / (c1 - c0);
+    const int e1 = min(G * D, (i - c0) * share);
+    for (int e = (i - c0 - 1) * share + threadIdx.x; e < e1; e += 128) {
+        const int h = e / D, d = e % D;
+        float M = -INFINITY;
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[(2 * c + (c == c0)) * HP + h]);
+        float L = 0.0f, O = 0.0f;
+        for (int c = c0; c <= c1; ++c) {
+            const size_t slot = static_cast<size_t>(2 * c + (c == c0)) * HP + h;
+            const float x = p.part_lse[slot];
+            const float w = x == M ? 1.0f : ex2_approx(x - M);
+            L += w;
+            O = fmaf(w, p.part_o[slot * D + d], O);
+        }
+        O /= L;
+        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[(head0 + h) * D + d] = O;
+        else static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(O);
+        if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
     }
-    O = L > 0.0f || L != L ? O / L : 0.0f;
-    if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[bh * D + threadIdx.x] = O;
-    else static_cast<__nv_bfloat16*>(p.o)[bh * D + threadIdx.x] = __float2bfloat16_rn(O);
-    if (threadIdx.x == 0) p.lse[bh] = L > 0.0f || L != L ? M + logf(L) : -INFINITY;
 }
 
-template <int D, int BITS>
-cudaError_t launch(const DecodeQuantParams& p, cudaStream_t stream) {
-    fa_decode_quant_split<D, BITS><<<dim3(p.B * p.H, p.splits), kSplitKeys, 0, stream>>>(p);
-    fa_decode_quant_combine<D><<<p.B * p.H, D, 0, stream>>>(p);
+template <int D, int BITS, int NT>
+cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream) {
+    using C = Cfg<D, BITS, NT>;
+    cudaError_t e = cudaFuncSetAttribute(fa_decode_quant_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    if (e != cudaSuccess) return e;
+    const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
+    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxCtas, C::kCtas * num_sms), units / kWarps)));
+    fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
+    if (grid > 1) fa_decode_quant_combine<D, NT><<<grid - 1, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-size_t workspace_bytes_of(int B, int H, int d) { return static_cast<size_t>(B) * H * kMaxSplits * (d + 1) * sizeof(float); }
+// 8-head tiles of a set: two (O takes NT D / 4 registers a thread) only where a second
+// one has heads, and D leaves room for it.
+int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+size_t part_bytes(int d, int nt) { return up256(static_cast<size_t>(2 * kMaxCtas) * 8 * nt * (d + 1) * sizeof(float)); }
+size_t workspace_bytes_of(int H, int Hkv, int d) {
+    return part_bytes(d, tiles_of(H / Hkv, d)) + up256(kMaxCtas * sizeof(int4)) + 256;
+}
 
 }  // namespace
+
+#ifdef FA_TEST_HOOKS
+cudaError_t quant_test_arm_skip_stage() {
+    const int one = 1;
+    return cudaMemcpyToSymbol(g_test_skip_quant, &one, sizeof(int));
+}
+#endif
+
 }  // namespace fa
 
 using namespace fa;
 
+#ifdef FA_TEST_HOOKS
+// Fault injection for the tests of the bounded waits (test build only): as
+// fa_test_inject_fault, for the quantised decode's copies.
+extern "C" int fa_test_inject_fault_quant(void) {
+    int* status = nullptr;
+    const int rc = prepare_device(&status);
+    if (rc != FA_OK) return rc;
+    return quant_test_arm_skip_stage() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+#endif
+
 extern "C" size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits) {
     if (kvq_check_pool(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
-    return workspace_bytes_of(B, H, d);
+    return workspace_bytes_of(H, Hkv, d);
 }
 
 extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
@@ -183,9 +764,18 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     if (!kvq_aligned(q, 16) || !kvq_aligned(kpages, 16) || !kvq_aligned(vpages, 16) || !kvq_aligned(o, 16) ||
         !kvq_aligned(lse, 4) || !kvq_aligned(block_table, 4) || !kvq_aligned(kv_lens, 4))
         return FA_ERR_INVALID_ARG;
-    if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(B, H, d)) return FA_ERR_WORKSPACE;
+    const int nt = tiles_of(H / Hkv, d);
     DecodeQuantParams p{};
+    p.sets = (H / Hkv + 8 * nt - 1) / (8 * nt);
+    p.cap = max_blocks * page_size;
+    // units are counted in int32; 16 keys is the shortest
+    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFFFFLL) return FA_ERR_INVALID_ARG;
+    if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(H, Hkv, d)) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
+    int dev = 0, num_sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return FA_ERR_CUDA;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.kpages = static_cast<const uint8_t*>(kpages);
     p.vpages = static_cast<const uint8_t*>(vpages);
@@ -193,21 +783,26 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.kv_lens = kv_lens;
     p.o = o;
     p.lse = lse;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_lse = p.part_o + static_cast<size_t>(B) * H * kMaxSplits * d;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = p.part_o + static_cast<size_t>(2 * kMaxCtas) * 8 * nt * d;
+    p.first = reinterpret_cast<int4*>(ws + part_bytes(d, nt));
+    p.plan = reinterpret_cast<int2*>(ws + part_bytes(d, nt) + up256(kMaxCtas * sizeof(int4)));
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
     p.num_pages = num_pages;
     p.page_shift = kvq_page_shift(page_size);
     p.max_blocks = max_blocks;
-    p.cap = max_blocks * page_size;
-    p.splits = (p.cap - 1) / kSplitKeys + 1 < kMaxSplits ? (p.cap - 1) / kSplitKeys + 1 : kMaxSplits;
     p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
     p.o_dtype = o_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (bits == 4) e = d == 64 ? launch<64, 4>(p, s) : d == 128 ? launch<128, 4>(p, s) : launch<256, 4>(p, s);
-    else e = d == 64 ? launch<64, 8>(p, s) : d == 128 ? launch<128, 8>(p, s) : launch<256, 8>(p, s);
+    if (d == 256) e = bits == 4 ? launch<256, 4, 1>(p, num_sms, s) : launch<256, 8, 1>(p, num_sms, s);
+    else if (d == 128 && nt == 1) e = bits == 4 ? launch<128, 4, 1>(p, num_sms, s) : launch<128, 8, 1>(p, num_sms, s);
+    else if (d == 128) e = bits == 4 ? launch<128, 4, 2>(p, num_sms, s) : launch<128, 8, 2>(p, num_sms, s);
+    else if (nt == 1) e = bits == 4 ? launch<64, 4, 1>(p, num_sms, s) : launch<64, 8, 1>(p, num_sms, s);
+    else e = bits == 4 ? launch<64, 4, 2>(p, num_sms, s) : launch<64, 8, 2>(p, num_sms, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
