@@ -26,10 +26,11 @@
 //
 // Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  The units
 // of the whole batch, in that order, are cut into equal runs, one a CTA; warp w of a
-// CTA takes every eighth unit of its run.  Each warp copies its own units into a ring of S
-// stages with 1-D bulk copies (a 16-token tile of K or of V is one run of bytes), so
-// nothing in the loop waits for another warp.  Where the run crosses into another
-// (sequence, head set), the eight warps merge their statistics and write the output,
+// CTA takes units u0 + w, u0 + w + NC, ... of its run.  Each of the NC compute warps has a
+// ring of S stages of its own, which a copy warp fills with 1-D bulk copies (a 16-token
+// tile of K or of V is one run of bytes): two of its lanes serve one compute warp, and
+// no compute warp waits for another in the loop.  Where the run crosses into another
+// (sequence, head set), the compute warps merge their statistics and write the output,
 // or, if the set's keys are shared with another CTA, a partial one that
 // fa_decode_quant_combine merges.  Every wait is bounded.
 #include <cuda_bf16.h>
@@ -46,9 +47,7 @@
 namespace fa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxCtas = 2 * 160;   // CTAs of a launch (bounds the workspace)
+constexpr int kMaxCtas = 160;   // CTAs of a launch (bounds the workspace)
 constexpr int kMergeDims = 64;      // dimensions merged at once
 constexpr float kRefBits = 6.0f;    // weights are 2^kRefBits times p s / 2^E at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
@@ -80,36 +79,76 @@ __device__ int g_test_skip_quant;
 template <int D, int BITS, int NT>
 struct Cfg {
     using F = KvqFormat<D, BITS>;
-    // two CTAs an SM need 128 registers a thread: O alone is NT D / 4 of them
-    static constexpr int kCtas = NT * D <= 128 ? 2 : 1;
-    static constexpr int kStageBudget = kCtas == 2 ? 10400 : 20800;  // bytes of a warp's ring
-    static constexpr int kBlocks = 8 * F::kTileBytes <= kStageBudget ? 2 : 1;  // tiles of a unit
+    // Compute warps.  With the copy warp they are 2, 3 or 4 warps for each of the SM's four
+    // schedulers, which leaves a thread 255, 168 or 128 registers; O alone takes NT D / 4.
+    static constexpr int NC = NT * D <= 64 ? 15 : NT * D <= 128 ? 11 : 7;
+    static constexpr int kThreads = 32 * (NC + 1);
+    static constexpr int kRingBudget = 184 * 1024;
+    static constexpr int kBlocks = 8 * F::kTileBytes * NC <= kRingBudget ? 2 : 1;  // tiles of a unit
     static constexpr int KT = 16 * kBlocks;
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kHalf;
-    static constexpr int S = kStageBudget / kStageBytes < 4 ? kStageBudget / kStageBytes : 4;
+    static constexpr int S = kRingBudget / (kStageBytes * NC) < 4 ? kRingBudget / (kStageBytes * NC) : 4;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
+    static constexpr int kZSteps = (F::kGroups + 3) / 4;  // products of lo, 4 groups each
     // shared memory
     static constexpr int kRedBytes = HP * kMergeDims * 4;  // of a warp; its score tile is kept there too
     static constexpr int kRingOff = 0;
-    static constexpr int kRedOff = kRingOff + kWarps * S * kStageBytes;
-    static constexpr int kZOff = kRedOff + kWarps * kRedBytes;           // [warp][head][group]
-    static constexpr int kMOff = kZOff + kWarps * HP * F::kGroups * 4;   // [warp][head] reference
-    static constexpr int kLOff = kMOff + kWarps * HP * 4;                // [warp][head] sum
-    static constexpr int kBarOff = kLOff + kWarps * HP * 4;
-    static constexpr int kMiscOff = kBarOff + kWarps * S * 8;
-    static constexpr int kBytes = kMiscOff + 64 + 128;
+    static constexpr int kRedOff = kRingOff + NC * S * kStageBytes;
+    static constexpr int kZOff = kRedOff + NC * kRedBytes;           // [warp][head][group]
+    static constexpr int kMOff = kZOff + NC * HP * F::kGroups * 4;   // [warp][head] reference
+    static constexpr int kLOff = kMOff + NC * HP * 4;                // [warp][head] sum
+    static constexpr int kBarOff = kLOff + NC * HP * 4;              // full[warp][S], empty[warp][S]
+    static constexpr int kMiscOff = kBarOff + 2 * NC * S * 8;
+    static constexpr int kBytes = kMiscOff + 32 * 4 + 128;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
     static_assert(S >= 2, "a stage is copied while another is read");
     static_assert(HP * kScoreStride * 4 <= kRedBytes, "a warp's scores fit its merge buffer");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two fp32 in one register pair, and one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 // fp16 pair, lo in bits 0-15
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -145,27 +184,32 @@ __device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len,
 // A place in the batch's order of units: the set that unit v belongs to.
 template <int KT>
 struct Cursor {
-    int b, hh, begin, n, len;  // sequence, set (KV head and head set), first unit, units, keys
+    int b, hkv, set, begin, n, len;  // sequence, KV head, head set, first unit, units, keys
     __device__ __forceinline__ void seek(const DecodeQuantParams& p, int v) {
         while (v >= begin + n) {
             begin += n;
-            if (++hh == p.Hkv * p.sets) {
-                hh = 0;
-                do {
-                    ++b;
-                    len = clamp_len(p.kv_lens[b], p.cap);
-                } while (len == 0);
-                n = units_of<KT>(len);
-            }
+            if (++set < p.sets) continue;
+            set = 0;
+            if (++hkv < p.Hkv) continue;
+            hkv = 0;
+            do {
+                ++b;
+                len = clamp_len(p.kv_lens[b], p.cap);
+            } while (len == 0);
+            n = units_of<KT>(len);
         }
     }
 };
 
+__device__ __forceinline__ void named_bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
+__global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
     using C = Cfg<D, BITS, NT>;
     using F = KvqFormat<D, BITS>;
-    constexpr int KT = C::KT, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
+    constexpr int KT = C::KT, S = C::S, NC = C::NC, kThreads = C::kThreads, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -173,14 +217,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     float* red_z = reinterpret_cast<float*>(smem + C::kZOff);
     float* red_m = reinterpret_cast<float*>(smem + C::kMOff);
     float* red_l = reinterpret_cast<float*>(smem + C::kLOff);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * S;
-    int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] abort, [1..4] first set, [8..15] scan
+    uint64_t* full_all = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [warp][S]
+    uint64_t* empty_all = full_all + NC * S;
+    int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] abort, [1..4] first set, [8..] scan
     volatile int* abort_flag = misc;
 
     // ---- plan: the number of units and the set of this CTA's first one
     if (tid == 0) *abort_flag = (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) ? 1 : 0;
-    if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&full[i], 1);
+    if (tid < NC * S) {
+        mbar_init(&full_all[tid], 2);   // the copies of K and of V
+        mbar_init(&empty_all[tid], 1);  // the warp that read the stage
         fence_barrier_init();
     }
     const int HH = p.Hkv * p.sets;
@@ -203,13 +249,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     if (*abort_flag) return;
     int total = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i <= NC; ++i) {
         if (i == warp) incl += total;
         total += misc[8 + i];
     }
     const int U = total * HH;
-    // a CTA has a unit for each of its warps before another one is used
-    const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / kWarps));
+    // a CTA has a unit for each of its compute warps before another one is used
+    const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / NC));
     const int cta = blockIdx.x;
     if (cta == 0 && tid == 0) *p.plan = make_int2(U, n_cta);
     if (cta >= n_cta) return;
@@ -244,79 +290,99 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         }
     }
     __syncthreads();
-    Cursor<KT> cur{misc[1], misc[2], misc[3], units_of<KT>(misc[4]), misc[4]};
-    Cursor<KT> ahead = cur;
+    Cursor<KT> cur{misc[1], misc[2] / p.sets, misc[2] % p.sets, misc[3], units_of<KT>(misc[4]), misc[4]};
     const int group = p.H / p.Hkv;
 
-    // ---- copies: this warp's units u0 + warp + 8 i, stage i % S
-    uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
-    const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    int v_load = u0 + warp;  // next unit to copy
-    int n_load = 0;          // units copied
-    int skipped = -1;
-    int page = -1, left = 0;  // of unit v_load: lane i's page and the unit's valid keys
-    auto look_up = [&]() {
-        if (v_load >= u1) return;
-        ahead.seek(p, v_load);
-        const int key0 = (v_load - ahead.begin) * KT;
-        left = min(KT, ahead.len - key0);
-        if (lane < NB && lane * 16 < left) {
-            page = p.block_table[static_cast<size_t>(ahead.b) * p.max_blocks + ((key0 + lane * 16) >> p.page_shift)];
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-                atomicCAS(p.status, 0, FA_ERR_PAGE);
-                page = 0;
-            }
-        }
-    };
-    auto issue = [&]() {
-        if (v_load >= u1) return;
-        const int s = n_load % S;
-        bool skip = false;
-#ifdef FA_TEST_HOOKS
-        int armed = 0;
-        if (lane == 0) armed = atomicExch(&g_test_skip_quant, 0);
-        skip = __shfl_sync(0xffffffffu, armed, 0) != 0;
-        if (skip) skipped = n_load;
-#endif
-        if (!skip) {
-            const int nb = (left + 15) / 16;
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(nb) * 2 * F::kTileBytes);
-            __syncwarp();
-            if (lane < nb) {
-                const int slot = ((v_load - ahead.begin) * KT + lane * 16) & ((1 << p.page_shift) - 1);
-                const size_t off = (static_cast<size_t>(page) * p.Hkv + ahead.hh / p.sets) * block_bytes +
-                                   static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
-                uint8_t* dst = ring + s * C::kStageBytes + lane * F::kTileBytes;
-                bulk_load(dst, p.kpages + off, F::kTileBytes, &full[s]);
-                bulk_load(dst + C::kHalf, p.vpages + off, F::kTileBytes, &full[s]);
-            }
-            __syncwarp();
-        }
-        ++n_load;
-        v_load += kWarps;
+    if (warp == NC) {
+        // ---------------- copy warp: lanes 2 w and 2 w + 1 copy K and V of compute warp w's units
+        const int w = lane >> 1;
+        uint64_t* full = full_all + w * S;
+        uint64_t* empty = empty_all + w * S;
+        const uint8_t* pages = lane & 1 ? p.vpages : p.kpages;
+        uint8_t* ring = smem + C::kRingOff + w * (S * C::kStageBytes) + (lane & 1) * C::kHalf;
+        const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
+        const size_t page_stride = block_bytes * p.Hkv;
+        const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
+        int v = w < NC ? u0 + w : u1;
+        int key = 0, left = 0, page0 = 0, page1 = 0;
+        auto look_up = [&]() {
+            if (v >= u1) return;
+            cur.seek(p, v);
+            key = (v - cur.begin) * KT;
+            left = min(KT, cur.len - key);
+            const int* entry = p.block_table + static_cast<size_t>(cur.b) * p.max_blocks + (key >> p.page_shift);
+            page0 = entry[0];
+            if (two && left > 16) page1 = entry[1];
+        };
         look_up();
-    };
-    look_up();
-    for (int i = 0; i < S - 1; ++i) issue();
+        int issued = 0, skipped = -1;
+        bool ok = true;
+        for (int round = 0, s = 0, phase = 1; __any_sync(0xffffffffu, ok && v < u1); ++round) {
+            bool live = ok && v < u1;
+            if (live && round >= S) ok = live = mbar_wait(&empty[s], phase, abort_flag, p.status);
+            if (live) issued = round + 1;
+#ifdef FA_TEST_HOOKS
+            int armed = 0;
+            if (lane == 0) armed = atomicExch(&g_test_skip_quant, 0);
+            if (__shfl_sync(0xffffffffu, armed, 0) != 0) {
+                skipped = round;
+                live = false;
+            }
+#endif
+            if (live) {
+                if (static_cast<unsigned>(page0) >= static_cast<unsigned>(p.num_pages)) {
+                    atomicCAS(p.status, 0, FA_ERR_PAGE);
+                    page0 = 0;
+                }
+                const int bytes = (NB == 1 || left <= 16 ? 1 : 2) * F::kTileBytes;
+                const size_t off = cur.hkv * block_bytes +
+                                   static_cast<size_t>((key & ((1 << p.page_shift) - 1)) / kKvqTile) * F::kTileBytes;
+                uint8_t* dst = ring + s * C::kStageBytes;
+                mbar_arrive_expect_tx(&full[s], bytes);
+                if (two && left > 16) {
+                    if (static_cast<unsigned>(page1) >= static_cast<unsigned>(p.num_pages)) {
+                        atomicCAS(p.status, 0, FA_ERR_PAGE);
+                        page1 = 0;
+                    }
+                    bulk_load(dst, pages + page0 * page_stride + off, F::kTileBytes, &full[s]);
+                    bulk_load(dst + F::kTileBytes, pages + page1 * page_stride + off, F::kTileBytes, &full[s]);
+                } else {
+                    bulk_load(dst, pages + page0 * page_stride + off, bytes, &full[s]);
+                }
+            }
+            if (v < u1) v += NC;
+            look_up();
+            if (++s == S) s = 0, phase ^= 1;
+        }
+        // every copy issued here lands before the shared memory goes away
+        for (int i = max(0, issued - S); i < issued; ++i)
+            if (i != skipped) mbar_wait_drain(&full[i % S], (i / S) & 1, p.status);
+        return;
+    }
 
-    // ---- the sets of this CTA's run
+    // ---------------- compute warps: the sets of this CTA's run
+    uint64_t* full = full_all + warp * S;
+    uint64_t* empty = empty_all + warp * S;
+    uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
     const int r = lane >> 2, t = lane & 3;
     float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
-    int v = u0 + warp, n_done = 0;
+    int v = u0 + warp, s = 0, phase = 0;
     bool ok = true;
     for (int at = u0; at < u1;) {
         cur.seek(p, at);
         const int end = min(u1, cur.begin + cur.n);
-        const int hkv = cur.hh / p.sets, h_in = (cur.hh - hkv * p.sets) * HP;
+        const int h_in = cur.set * HP;
         const int G = min(HP, group - h_in);  // heads of the set
-        const size_t head0 = static_cast<size_t>(cur.b) * p.H + hkv * group + h_in;
+        const size_t head0 = static_cast<size_t>(cur.b) * p.H + cur.hkv * group + h_in;
 
         float o[NT][D / 16][4];
-        float oz[NT][NG], m[NT], l[NT];
+        uint64_t oz[NT][NG];  // sums of p lo over the thread's even and odd keys
+        float m[NT], l[NT];
         int E = -1000;
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
-        float qs[NT][NG][2], A[NT][2];  // of the score fragment's heads 2 t, 2 t + 1
+        uint32_t qz[NT][C::kZSteps][2];  // sums of q over a group, as the B operand of the lo product
+        float A[NT][2];                  // of the score fragment's heads 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = -INFINITY;
@@ -327,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             const int h = nt * 8 + r;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                oz[nt][g] = 0.0f;
+                oz[nt][g] = 0;
                 raw[g] = h < G ? *reinterpret_cast<const uint4*>(p.q + (head0 + h) * D + g * kKvqGroup + t * 8)
                                : make_uint4(0, 0, 0, 0);
             }
@@ -344,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             const int e = max(static_cast<int>(big >> 23) - 127, -100);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);  // 2^(14 - e)
             const float a_own = ldexpf(p.scale_log2, 10 + e);                             // undoes it and the codes' 2^-24
+            float own = 0.0f, own4 = 0.0f;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float f[8], sum = 0.0f;
@@ -372,21 +439,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum *= p.scale_log2;
-                qs[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * t);
-                qs[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+                if (g == t) own = sum;
+                if (g == t + 4) own4 = sum;
+            }
+            // thread t's slots of the 16 are group t (or t + 4): the sum in three bf16, which hold all of its 24 bits
+#pragma unroll
+            for (int zs = 0; zs < C::kZSteps; ++zs) {
+                const float x = zs ? own4 : own;
+                const float hi = round_bf16(x), mid = round_bf16(x - hi);
+                qz[nt][zs][0] = pack_bf16x2(hi, mid);
+                qz[nt][zs][1] = pack_bf16x2(x - hi - mid, 0.0f);
             }
             A[nt][0] = __shfl_sync(0xffffffffu, a_own, 8 * t);
             A[nt][1] = __shfl_sync(0xffffffffu, a_own, 8 * t + 4);
         }
 
-        for (; v < end; v += kWarps, ++n_done) {
-            if (ok) issue();
-            const int s = n_done % S;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (n_done / S) & 1, abort_flag, p.status));
+        const int last = cur.begin + cur.n - 1;  // the only unit that may be short
+        for (; v < end; v += NC) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], phase, abort_flag, p.status));
             if (!ok) continue;
             uint8_t* ks = ring + s * C::kStageBytes;
             uint8_t* vs = ks + C::kHalf;
-            const int valid = min(KT, cur.len - (v - cur.begin) * KT);
+            const int valid = v == last ? cur.len - (v - cur.begin) * KT : KT;
             const int nb = (valid + 15) / 16;
             if (valid < KT) {
                 // Slots past the last key may hold anything: their V parameters become zero
@@ -413,6 +487,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x1[nt][i] = x2[nt][i] = 0.0f;
+                // x2 = sum over groups of lo sum(q): lo is the A operand, twice in each of thread t's registers
+#pragma unroll
+                for (int zs = 0; zs < C::kZSteps; ++zs) {
+                    const int at_z = F::kParamOff + r * F::kParamBytes + (NG < 4 ? t % NG : zs * 4 + t) * 4;
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(kt + at_z);
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t*>(kt + at_z + 8 * F::kParamBytes);
+                    const uint32_t z0 = __byte_perm(w0, w0, 0x1010), z1 = __byte_perm(w1, w1, 0x1010);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_bf16(x2[nt], z0, z1, z0, z1, qz[nt][zs][0], qz[nt][zs][1]);
+                }
 #pragma unroll
                 for (int pl = 0; pl < F::kPlanes; ++pl) {
                     constexpr int W = F::kPlaneBytes / 16;  // words of a thread and row
@@ -423,8 +507,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     for (int gp = 0; gp < PG; ++gp) {
                         const int g = pl * PG + gp;
                         float acc[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
 #pragma unroll
                         for (int st = 0; st < 2; ++st) {
                             uint32_t a0, a1, a2, a3;
@@ -438,20 +520,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                                 a2 = (w0 >> 8) & 0x00FF00FFu, a3 = (w1 >> 8) & 0x00FF00FFu;
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2 * st], qb[nt][g][2 * st + 1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (st == 0) mma_f16_zero(acc[nt], a0, a1, a2, a3, qb[nt][g][0], qb[nt][g][1]);
+                                else mma_f16(acc[nt], a0, a1, a2, a3, qb[nt][g][2], qb[nt][g][3]);
+                            }
                         }
-                        const float s0 = s_of(par0[g]), s1 = s_of(par1[g]), z0 = lo_of(par0[g]), z1 = lo_of(par1[g]);
+                        const float s0 = s_of(par0[g]), s1 = s_of(par1[g]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             x1[nt][0] = fmaf(s0, acc[nt][0], x1[nt][0]);
                             x1[nt][1] = fmaf(s0, acc[nt][1], x1[nt][1]);
                             x1[nt][2] = fmaf(s1, acc[nt][2], x1[nt][2]);
                             x1[nt][3] = fmaf(s1, acc[nt][3], x1[nt][3]);
-                            x2[nt][0] = fmaf(z0, qs[nt][g][0], x2[nt][0]);
-                            x2[nt][1] = fmaf(z0, qs[nt][g][1], x2[nt][1]);
-                            x2[nt][2] = fmaf(z1, qs[nt][g][0], x2[nt][2]);
-                            x2[nt][3] = fmaf(z1, qs[nt][g][1], x2[nt][3]);
                         }
                     }
                 }
@@ -512,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     l[nt] *= alpha;
                     const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) oz[nt][g] *= alpha;
+                    for (int g = 0; g < NG; ++g) oz[nt][g] = mul2(oz[nt][g], pair(alpha, alpha));
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                         o[nt][j][0] *= al0;
@@ -545,12 +625,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* uu = u[nt] + 4 * kb;
+                        const uint64_t u01 = pair(uu[0], uu[1]), u23 = pair(uu[2], uu[3]);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
-                            wb[nt][g][0] = pack_f16x2(uu[0] * s_of(par[0][g]), uu[1] * s_of(par[1][g]));
-                            wb[nt][g][1] = pack_f16x2(uu[2] * s_of(par[2][g]), uu[3] * s_of(par[3][g]));
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) oz[nt][g] = fmaf(uu[i], lo_of(par[i][g]), oz[nt][g]);
+                            const float2 w01 = unpair(mul2(u01, pair(s_of(par[0][g]), s_of(par[1][g]))));
+                            const float2 w23 = unpair(mul2(u23, pair(s_of(par[2][g]), s_of(par[3][g]))));
+                            wb[nt][g][0] = pack_f16x2(w01.x, w01.y);
+                            wb[nt][g][1] = pack_f16x2(w23.x, w23.y);
+                            oz[nt][g] = fma2(u01, pair(lo_of(par[0][g]), lo_of(par[1][g])), oz[nt][g]);
+                            oz[nt][g] = fma2(u23, pair(lo_of(par[2][g]), lo_of(par[3][g])), oz[nt][g]);
                         }
                     }
                 }
@@ -590,9 +673,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 }
             }
             __syncwarp();  // the stage and the scores may be overwritten
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == S) s = 0, phase ^= 1;
         }
 
-        // ---- merge the eight warps: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of heads 2 t, 2 t + 1
+        // ---- merge the warps: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of heads 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
@@ -604,9 +689,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                oz[nt][g] += __shfl_xor_sync(0xffffffffu, oz[nt][g], 1);
-                oz[nt][g] += __shfl_xor_sync(0xffffffffu, oz[nt][g], 2);
-                if (t == 0) red_z[at_h * NG + g] = oz[nt][g];
+                const float2 two = unpair(oz[nt][g]);
+                float z = two.x + two.y;
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                if (t == 0) red_z[at_h * NG + g] = z;
             }
         }
         const bool whole = at == cur.begin && end == cur.begin + cur.n;
@@ -628,16 +715,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                             make_float4(o0[c] * kUp, o0[c + 2] * kUp1, o1[c] * kUp, o1[c + 2] * kUp1);
                     }
                 }
-            __syncthreads();
+            named_bar_sync(1, 32 * NC);
             const bool aborted = *abort_flag != 0;
-            for (int e = tid; !aborted && e < G * kMergeDims; e += kThreads) {
+            for (int e = tid; !aborted && e < G * kMergeDims; e += 32 * NC) {
                 const int h = e / kMergeDims, c = e % kMergeDims, d = md * kMergeDims + c;
                 float M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red_m[w * HP + h]);
+                for (int w = 0; w < NC; ++w) M = fmaxf(M, red_m[w * HP + h]);
                 float L = 0.0f, O = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = 0; w < NC; ++w) {
                     const float mw = red_m[w * HP + h];
                     // no finite score: nothing seen, or only NaN and -inf (then l and O say so)
                     const float wt = mw == M ? 1.0f : ex2_approx(mw - M);
@@ -654,13 +741,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     if (d == 0) p.part_lse[slot * HP + h] = M - kRefBits + log2f(L);
                 }
             }
-            __syncthreads();
+            named_bar_sync(1, 32 * NC);
         }
         at = end;
     }
-    // after a wait that ran out: every copy issued here lands before the shared memory goes away
-    for (int i = n_done > 0 && !ok ? max(0, n_load - S) : n_load; i < n_load; ++i)
-        if (i != skipped) mbar_wait_drain(&full[i % S], (i / S) & 1, p.status);
 }
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
@@ -704,11 +788,12 @@ __global__ void __launch_bounds__(128) fa_decode_quant_combine(const __grid_cons
 template <int D, int BITS, int NT>
 cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream) {
     using C = Cfg<D, BITS, NT>;
+    constexpr int NC = C::NC;
     cudaError_t e = cudaFuncSetAttribute(fa_decode_quant_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
     if (e != cudaSuccess) return e;
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
-    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxCtas, C::kCtas * num_sms), units / kWarps)));
-    fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
+    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxCtas, num_sms), units / NC)));
+    fa_decode_quant_split<D, BITS, NT><<<grid, C::kThreads, C::kBytes, stream>>>(p);
     if (grid > 1) fa_decode_quant_combine<D, NT><<<grid - 1, 128, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -768,8 +853,8 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     DecodeQuantParams p{};
     p.sets = (H / Hkv + 8 * nt - 1) / (8 * nt);
     p.cap = max_blocks * page_size;
-    // units are counted in int32; 16 keys is the shortest
-    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFFFFLL) return FA_ERR_INVALID_ARG;
+    // units are counted in int32, a little past the last one too; 16 keys is the shortest
+    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(H, Hkv, d)) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;
