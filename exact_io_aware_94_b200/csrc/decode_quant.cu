@@ -26,13 +26,13 @@
 //
 // Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  The units
 // of the whole batch, in that order, are cut into equal runs, one a CTA; warp w of a
-// CTA takes units u0 + w, u0 + w + NC, ... of its run.  Each of the NC compute warps has a
-// ring of S stages of its own, which a copy warp fills with 1-D bulk copies (a 16-token
-// tile of K or of V is one run of bytes): two of its lanes serve one compute warp, and
-// no compute warp waits for another in the loop.  Where the run crosses into another
-// (sequence, head set), the compute warps merge their statistics and write the output,
-// or, if the set's keys are shared with another CTA, a partial one that
-// fa_decode_quant_combine merges.  Every wait is bounded.
+// CTA takes units u0 + w, u0 + w + 4, ... of its run.  Each of the four warps copies its own
+// units into a ring of S stages of its own with 16-byte asynchronous copies (a 16-token
+// tile of K or of V is one run of bytes), so no warp waits for another in the loop.
+// Where the run crosses into another (sequence, head set), the warps merge their
+// statistics and write the output, or, if the set's keys are shared with another CTA, a
+// partial one that fa_decode_quant_combine merges.  An SM holds several CTAs, so that one
+// computes while another starts, merges or ends.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,7 +47,12 @@
 namespace fa {
 namespace {
 
-constexpr int kMaxCtas = 160;   // CTAs of a launch (bounds the workspace)
+constexpr int kMaxSms = 160;        // bounds the CTAs of a launch and so the workspace
+constexpr int NC = 4;               // warps of a CTA
+constexpr int kThreads = 32 * NC;
+// CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone takes nt d / 4.
+__host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
+__host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
 constexpr int kMergeDims = 64;      // dimensions merged at once
 constexpr float kRefBits = 6.0f;    // weights are 2^kRefBits times p s / 2^E at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
@@ -70,20 +75,11 @@ struct DecodeQuantParams {
     int o_dtype;
 };
 
-#ifdef FA_TEST_HOOKS
-// One-shot fault (test build only): the next stage a warp would fill gets neither its
-// expected byte count nor its copies, so the warp's wait for it runs out.
-__device__ int g_test_skip_quant;
-#endif
-
 template <int D, int BITS, int NT>
 struct Cfg {
     using F = KvqFormat<D, BITS>;
-    // Compute warps.  With the copy warp they are 2, 3 or 4 warps for each of the SM's four
-    // schedulers, which leaves a thread 255, 168 or 128 registers; O alone takes NT D / 4.
-    static constexpr int NC = NT * D <= 64 ? 15 : NT * D <= 128 ? 11 : 7;
-    static constexpr int kThreads = 32 * (NC + 1);
-    static constexpr int kRingBudget = 184 * 1024;
+    static constexpr int kCtas = ctas_per_sm(D, NT);
+    static constexpr int kRingBudget = (kCtas == 4 ? 46 : kCtas == 3 ? 62 : 84) * 1024;  // of a CTA
     static constexpr int kBlocks = 8 * F::kTileBytes * NC <= kRingBudget ? 2 : 1;  // tiles of a unit
     static constexpr int KT = 16 * kBlocks;
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
@@ -99,10 +95,9 @@ struct Cfg {
     static constexpr int kZOff = kRedOff + NC * kRedBytes;           // [warp][head][group]
     static constexpr int kMOff = kZOff + NC * HP * F::kGroups * 4;   // [warp][head] reference
     static constexpr int kLOff = kMOff + NC * HP * 4;                // [warp][head] sum
-    static constexpr int kBarOff = kLOff + NC * HP * 4;              // full[warp][S], empty[warp][S]
-    static constexpr int kMiscOff = kBarOff + 2 * NC * S * 8;
+    static constexpr int kMiscOff = kLOff + NC * HP * 4;
     static constexpr int kBytes = kMiscOff + 32 * 4 + 128;
-    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+    static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of a CTA");
     static_assert(S >= 2, "a stage is copied while another is read");
     static_assert(HP * kScoreStride * 4 <= kRedBytes, "a warp's scores fit its merge buffer");
 };
@@ -201,15 +196,20 @@ struct Cursor {
     }
 };
 
-__device__ __forceinline__ void named_bar_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups of this thread have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
+__global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
     using C = Cfg<D, BITS, NT>;
     using F = KvqFormat<D, BITS>;
-    constexpr int KT = C::KT, S = C::S, NC = C::NC, kThreads = C::kThreads, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
+    constexpr int KT = C::KT, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -217,18 +217,10 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
     float* red_z = reinterpret_cast<float*>(smem + C::kZOff);
     float* red_m = reinterpret_cast<float*>(smem + C::kMOff);
     float* red_l = reinterpret_cast<float*>(smem + C::kLOff);
-    uint64_t* full_all = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [warp][S]
-    uint64_t* empty_all = full_all + NC * S;
-    int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] abort, [1..4] first set, [8..] scan
-    volatile int* abort_flag = misc;
+    int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] exit, [1..4] first set, [8..] scan
 
     // ---- plan: the number of units and the set of this CTA's first one
-    if (tid == 0) *abort_flag = (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) ? 1 : 0;
-    if (tid < NC * S) {
-        mbar_init(&full_all[tid], 2);   // the copies of K and of V
-        mbar_init(&empty_all[tid], 1);  // the warp that read the stage
-        fence_barrier_init();
-    }
+    if (tid == 0) misc[0] = (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) ? 1 : 0;
     const int HH = p.Hkv * p.sets;
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -246,10 +238,10 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
     }
     if (lane == 31) misc[8 + warp] = incl;
     __syncthreads();
-    if (*abort_flag) return;
+    if (misc[0]) return;
     int total = 0;
 #pragma unroll
-    for (int i = 0; i <= NC; ++i) {
+    for (int i = 0; i < NC; ++i) {
         if (i == warp) incl += total;
         total += misc[8 + i];
     }
@@ -293,81 +285,74 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
     Cursor<KT> cur{misc[1], misc[2] / p.sets, misc[2] % p.sets, misc[3], units_of<KT>(misc[4]), misc[4]};
     const int group = p.H / p.Hkv;
 
-    if (warp == NC) {
-        // ---------------- copy warp: lanes 2 w and 2 w + 1 copy K and V of compute warp w's units
-        const int w = lane >> 1;
-        uint64_t* full = full_all + w * S;
-        uint64_t* empty = empty_all + w * S;
-        const uint8_t* pages = lane & 1 ? p.vpages : p.kpages;
-        uint8_t* ring = smem + C::kRingOff + w * (S * C::kStageBytes) + (lane & 1) * C::kHalf;
-        const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-        const size_t page_stride = block_bytes * p.Hkv;
-        const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
-        int v = w < NC ? u0 + w : u1;
-        int key = 0, left = 0, page0 = 0, page1 = 0;
-        auto look_up = [&]() {
-            if (v >= u1) return;
-            cur.seek(p, v);
-            key = (v - cur.begin) * KT;
-            left = min(KT, cur.len - key);
-            const int* entry = p.block_table + static_cast<size_t>(cur.b) * p.max_blocks + (key >> p.page_shift);
-            page0 = entry[0];
-            if (two && left > 16) page1 = entry[1];
-        };
-        look_up();
-        int issued = 0, skipped = -1;
-        bool ok = true;
-        for (int round = 0, s = 0, phase = 1; __any_sync(0xffffffffu, ok && v < u1); ++round) {
-            bool live = ok && v < u1;
-            if (live && round >= S) ok = live = mbar_wait(&empty[s], phase, abort_flag, p.status);
-            if (live) issued = round + 1;
-#ifdef FA_TEST_HOOKS
-            int armed = 0;
-            if (lane == 0) armed = atomicExch(&g_test_skip_quant, 0);
-            if (__shfl_sync(0xffffffffu, armed, 0) != 0) {
-                skipped = round;
-                live = false;
-            }
-#endif
-            if (live) {
-                if (static_cast<unsigned>(page0) >= static_cast<unsigned>(p.num_pages)) {
-                    atomicCAS(p.status, 0, FA_ERR_PAGE);
-                    page0 = 0;
-                }
-                const int bytes = (NB == 1 || left <= 16 ? 1 : 2) * F::kTileBytes;
-                const size_t off = cur.hkv * block_bytes +
-                                   static_cast<size_t>((key & ((1 << p.page_shift) - 1)) / kKvqTile) * F::kTileBytes;
-                uint8_t* dst = ring + s * C::kStageBytes;
-                mbar_arrive_expect_tx(&full[s], bytes);
-                if (two && left > 16) {
-                    if (static_cast<unsigned>(page1) >= static_cast<unsigned>(p.num_pages)) {
-                        atomicCAS(p.status, 0, FA_ERR_PAGE);
-                        page1 = 0;
-                    }
-                    bulk_load(dst, pages + page0 * page_stride + off, F::kTileBytes, &full[s]);
-                    bulk_load(dst + F::kTileBytes, pages + page1 * page_stride + off, F::kTileBytes, &full[s]);
-                } else {
-                    bulk_load(dst, pages + page0 * page_stride + off, bytes, &full[s]);
-                }
-            }
-            if (v < u1) v += NC;
-            look_up();
-            if (++s == S) s = 0, phase ^= 1;
-        }
-        // every copy issued here lands before the shared memory goes away
-        for (int i = max(0, issued - S); i < issued; ++i)
-            if (i != skipped) mbar_wait_drain(&full[i % S], (i / S) & 1, p.status);
-        return;
-    }
-
-    // ---------------- compute warps: the sets of this CTA's run
-    uint64_t* full = full_all + warp * S;
-    uint64_t* empty = empty_all + warp * S;
+    // ---- copies: this warp's units u0 + warp + NC i, stage i % S
     uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
+    const uint32_t ring_lane = smem_u32(ring) + lane * 16;
+    const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
+    const size_t page_stride = block_bytes * p.Hkv;
+    const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
+    Cursor<KT> ahead = cur;
+    int v_load = u0 + warp, s_load = 0;
+    int key = 0, left = 0, page0 = 0, page1 = 0;  // of unit v_load
+    auto look_up = [&]() {
+        if (v_load >= u1) return;
+        ahead.seek(p, v_load);
+        key = (v_load - ahead.begin) * KT;
+        left = ahead.len - key;
+        const int* entry = p.block_table + static_cast<size_t>(ahead.b) * p.max_blocks + (key >> p.page_shift);
+        page0 = entry[0];
+        if (two && left > 16) page1 = entry[1];
+    };
+    auto issue = [&]() {
+        if (v_load < u1) {
+            if (static_cast<unsigned>(page0) >= static_cast<unsigned>(p.num_pages)) {
+                atomicCAS(p.status, 0, FA_ERR_PAGE);
+                page0 = 0;
+            }
+            const size_t off = page0 * page_stride + (ahead.hkv * block_bytes + lane * 16) +
+                               static_cast<size_t>((key & ((1 << p.page_shift) - 1)) / kKvqTile) * F::kTileBytes;
+            const uint8_t* k0 = p.kpages + off;
+            const uint8_t* v0 = p.vpages + off;
+            const uint32_t dst = ring_lane + s_load * C::kStageBytes;
+            if (!two && left >= KT) {  // one run of bytes
+#pragma unroll
+                for (int i = 0; i < C::kHalf; i += 512) {
+                    if (i + 512 <= C::kHalf || lane * 16 < C::kHalf - i) {
+                        copy16(dst + i, k0 + i);
+                        copy16(dst + C::kHalf + i, v0 + i);
+                    }
+                }
+            } else {
+                for (int kb = 0; kb < NB && kb * 16 < left; ++kb) {
+                    if (two && kb == 1) {
+                        if (static_cast<unsigned>(page1) >= static_cast<unsigned>(p.num_pages)) {
+                            atomicCAS(p.status, 0, FA_ERR_PAGE);
+                            page1 = 0;
+                        }
+                        const size_t to = page1 * page_stride - page0 * page_stride - F::kTileBytes;
+                        k0 += to;
+                        v0 += to;
+                    }
+                    for (int i = kb * F::kTileBytes; lane * 16 + i < (kb + 1) * F::kTileBytes; i += 512) {
+                        copy16(dst + i, k0 + i);
+                        copy16(dst + C::kHalf + i, v0 + i);
+                    }
+                }
+            }
+            v_load += NC;
+            s_load = s_load + 1 == S ? 0 : s_load + 1;
+            look_up();
+        }
+        copy_commit();
+    };
+    look_up();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue();
+
+    // ---- the sets of this CTA's run
     const int r = lane >> 2, t = lane & 3;
     float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
-    int v = u0 + warp, s = 0, phase = 0;
-    bool ok = true;
+    int v = u0 + warp, s = 0;
     for (int at = u0; at < u1;) {
         cur.seek(p, at);
         const int end = min(u1, cur.begin + cur.n);
@@ -456,8 +441,9 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
 
         const int last = cur.begin + cur.n - 1;  // the only unit that may be short
         for (; v < end; v += NC) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[s], phase, abort_flag, p.status));
-            if (!ok) continue;
+            issue();
+            copy_wait<S - 1>();
+            __syncwarp();
             uint8_t* ks = ring + s * C::kStageBytes;
             uint8_t* vs = ks + C::kHalf;
             const int valid = v == last ? cur.len - (v - cur.begin) * KT : KT;
@@ -472,7 +458,6 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                                                      (key % 16) * F::kParamBytes + (i % NG) * 4) = 0u;
                 }
                 __syncwarp();
-                fence_proxy_async_smem();  // before the stage's next bulk copy
             }
             // ---- scores
 #pragma unroll
@@ -673,8 +658,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                 }
             }
             __syncwarp();  // the stage and the scores may be overwritten
-            if (lane == 0) mbar_arrive(&empty[s]);
-            if (++s == S) s = 0, phase ^= 1;
+            s = s + 1 == S ? 0 : s + 1;
         }
 
         // ---- merge the warps: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of heads 2 t, 2 t + 1
@@ -715,9 +699,8 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                             make_float4(o0[c] * kUp, o0[c + 2] * kUp1, o1[c] * kUp, o1[c + 2] * kUp1);
                     }
                 }
-            named_bar_sync(1, 32 * NC);
-            const bool aborted = *abort_flag != 0;
-            for (int e = tid; !aborted && e < G * kMergeDims; e += 32 * NC) {
+            __syncthreads();
+            for (int e = tid; e < G * kMergeDims; e += kThreads) {
                 const int h = e / kMergeDims, c = e % kMergeDims, d = md * kMergeDims + c;
                 float M = -INFINITY;
 #pragma unroll
@@ -741,18 +724,23 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                     if (d == 0) p.part_lse[slot * HP + h] = M - kRefBits + log2f(L);
                 }
             }
-            named_bar_sync(1, 32 * NC);
+            __syncthreads();
         }
         at = end;
     }
 }
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
-// CTAs has P - 1 such blocks, each of which merges a share of its outputs.
+// CTAs has P - 1 such blocks, each of which merges a share of its outputs: a warp finds
+// the P weights of a head, then the block's threads share the outputs and the parts.
+constexpr int kCombineThreads = 128;
 template <int D, int NT>
-__global__ void __launch_bounds__(128) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
+__global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
     constexpr int HP = 8 * NT;
-    if (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) return;
+    __shared__ float s_w[HP][max_ctas(D, NT)];  // of part c0 + i, normalised
+    __shared__ float s_o[kCombineThreads];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (*static_cast<volatile const int*>(p.status) == FA_ERR_TIMEOUT) return;
     const int2 plan = *p.plan;
     const int i = blockIdx.x + 1;
     if (i >= plan.y) return;
@@ -760,41 +748,73 @@ __global__ void __launch_bounds__(128) fa_decode_quant_combine(const __grid_cons
     const int4 set = p.first[i];  // sequence, set, first unit, units
     if (set.z == static_cast<int>(U * i / n_cta)) return;  // starts with the CTA
     const int c0 = static_cast<int>(((set.z + 1LL) * n_cta - 1) / U);
-    const int c1 = static_cast<int>((static_cast<long long>(set.z + set.w) * n_cta - 1) / U);
+    const int P = static_cast<int>((static_cast<long long>(set.z + set.w) * n_cta - 1) / U) - c0 + 1;
     const int hkv = set.y / p.sets, group = p.H / p.Hkv, h_in = (set.y - hkv * p.sets) * HP;
     const int G = min(HP, group - h_in);
     const size_t head0 = static_cast<size_t>(set.x) * p.H + hkv * group + h_in;
-    const int share = (G * D + c1 - c0 - 1) / (c1 - c0);
-    const int e1 = min(G * D, (i - c0) * share);
-    for (int e = (i - c0 - 1) * share + threadIdx.x; e < e1; e += 128) {
-        const int h = e / D, d = e % D;
+    // outputs e0 to e1 of the set's G D
+    const int share = (G * D + P - 2) / (P - 1);
+    const int e0 = (i - c0 - 1) * share, e1 = min(G * D, e0 + share);
+    if (e0 >= e1) return;
+    // part i is the last one CTA c0 wrote (slot 2 c0 + 1), or the first one of a later CTA
+    auto slot = [&](int c) { return static_cast<size_t>(2 * (c0 + c) + (c == 0)) * HP; };
+    for (int h = e0 / D + warp; h <= (e1 - 1) / D; h += kCombineThreads / 32) {
         float M = -INFINITY;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_lse[(2 * c + (c == c0)) * HP + h]);
-        float L = 0.0f, O = 0.0f;
-        for (int c = c0; c <= c1; ++c) {
-            const size_t slot = static_cast<size_t>(2 * c + (c == c0)) * HP + h;
-            const float x = p.part_lse[slot];
-            const float w = x == M ? 1.0f : ex2_approx(x - M);
-            L += w;
-            O = fmaf(w, p.part_o[slot * D + d], O);
+        for (int c = lane; c < P; c += 32) {
+            s_w[h][c] = p.part_lse[slot(c) + h];
+            M = fmaxf(M, s_w[h][c]);
         }
-        O /= L;
-        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[(head0 + h) * D + d] = O;
-        else static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(O);
-        if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.0f;
+        for (int c = lane; c < P; c += 32) {
+            const float w = s_w[h][c] == M ? 1.0f : ex2_approx(s_w[h][c] - M);
+            s_w[h][c] = w;
+            L += w;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int c = lane; c < P; c += 32) s_w[h][c] /= L;
+        if (lane == 0 && h * D >= e0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+    auto store = [&](int e, float x) {
+        const size_t at = (head0 + e / D) * D + e % D;
+        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[at] = x;
+        else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
+    };
+    // W columns of outputs, kCombineThreads / W threads each
+    int W = kCombineThreads;
+    while (W > 4 && W / 2 >= share) W /= 2;
+    const int col = tid % W, row = tid / W, rows = kCombineThreads / W;
+    for (int eb = e0; eb < e1; eb += W) {
+        const int e = min(eb + col, e1 - 1), h = e / D, d = e % D;
+        float x = 0.0f;
+#pragma unroll 8
+        for (int c = row; c < P; c += rows) x = fmaf(s_w[h][c], p.part_o[(slot(c) + h) * D + d], x);
+        if (rows > 1) {
+            s_o[tid] = x;
+            __syncthreads();
+            for (int k = rows / 2; k > 0; k /= 2) {
+                if (row < k) s_o[tid] += s_o[tid + k * W];
+                __syncthreads();
+            }
+            x = s_o[col];
+        }
+        if (row == 0 && eb + col < e1) store(e, x);
+        __syncthreads();
     }
 }
 
 template <int D, int BITS, int NT>
 cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream) {
     using C = Cfg<D, BITS, NT>;
-    constexpr int NC = C::NC;
     cudaError_t e = cudaFuncSetAttribute(fa_decode_quant_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
     if (e != cudaSuccess) return e;
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
-    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxCtas, num_sms), units / NC)));
-    fa_decode_quant_split<D, BITS, NT><<<grid, C::kThreads, C::kBytes, stream>>>(p);
-    if (grid > 1) fa_decode_quant_combine<D, NT><<<grid - 1, 128, 0, stream>>>(p);
+    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
+    fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
+    if (grid > 1) fa_decode_quant_combine<D, NT><<<grid - 1, kCombineThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -803,34 +823,17 @@ cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream)
 int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-size_t part_bytes(int d, int nt) { return up256(static_cast<size_t>(2 * kMaxCtas) * 8 * nt * (d + 1) * sizeof(float)); }
+size_t part_bytes(int d, int nt) { return up256(static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * (d + 1) * sizeof(float)); }
 size_t workspace_bytes_of(int H, int Hkv, int d) {
-    return part_bytes(d, tiles_of(H / Hkv, d)) + up256(kMaxCtas * sizeof(int4)) + 256;
+    const int nt = tiles_of(H / Hkv, d);
+    return part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)) + 256;
 }
 
 }  // namespace
 
-#ifdef FA_TEST_HOOKS
-cudaError_t quant_test_arm_skip_stage() {
-    const int one = 1;
-    return cudaMemcpyToSymbol(g_test_skip_quant, &one, sizeof(int));
-}
-#endif
-
 }  // namespace fa
 
 using namespace fa;
-
-#ifdef FA_TEST_HOOKS
-// Fault injection for the tests of the bounded waits (test build only): as
-// fa_test_inject_fault, for the quantised decode's copies.
-extern "C" int fa_test_inject_fault_quant(void) {
-    int* status = nullptr;
-    const int rc = prepare_device(&status);
-    if (rc != FA_OK) return rc;
-    return quant_test_arm_skip_stage() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-}
-#endif
 
 extern "C" size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits) {
     if (kvq_check_pool(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
@@ -870,9 +873,9 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.lse = lse;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
-    p.part_lse = p.part_o + static_cast<size_t>(2 * kMaxCtas) * 8 * nt * d;
+    p.part_lse = p.part_o + static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * d;
     p.first = reinterpret_cast<int4*>(ws + part_bytes(d, nt));
-    p.plan = reinterpret_cast<int2*>(ws + part_bytes(d, nt) + up256(kMaxCtas * sizeof(int4)));
+    p.plan = reinterpret_cast<int2*>(ws + part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)));
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
