@@ -87,12 +87,17 @@ struct Cfg {
     static constexpr int S = kRingBudget / (kStageBytes * NC) < 4 ? kRingBudget / (kStageBytes * NC) : 4;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
+    // V's s and lo of a unit in fp32, [tile][group][s, lo][16 keys in score order]; 32 words a group would put
+    // a warp's stores of two groups on the same banks
+    static constexpr int kParStride = 40;
+    static constexpr int kParBytes = kBlocks * F::kGroups * kParStride * 4;
     static constexpr int kZSteps = (F::kGroups + 3) / 4;  // products of lo, 4 groups each
     // shared memory
     static constexpr int kRedBytes = HP * kMergeDims * 4;  // of a warp; its score tile is kept there too
     static constexpr int kRingOff = 0;
     static constexpr int kRedOff = kRingOff + NC * S * kStageBytes;
-    static constexpr int kZOff = kRedOff + NC * kRedBytes;           // [warp][head][group]
+    static constexpr int kParOff = kRedOff + NC * kRedBytes;
+    static constexpr int kZOff = kParOff + NC * kParBytes;           // [warp][head][group]
     static constexpr int kMOff = kZOff + NC * HP * F::kGroups * 4;   // [warp][head] reference
     static constexpr int kLOff = kMOff + NC * HP * 4;                // [warp][head] sum
     static constexpr int kMiscOff = kLOff + NC * HP * 4;
@@ -123,6 +128,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 // Two fp32 in one register pair, and one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -289,17 +301,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
     const uint32_t ring_lane = smem_u32(ring) + lane * 16;
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    const size_t page_stride = block_bytes * p.Hkv;
+    const uint32_t page_stride16 = static_cast<uint32_t>(block_bytes * p.Hkv / 16);
     const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
     Cursor<KT> ahead = cur;
     int v_load = u0 + warp, s_load = 0;
     int key = 0, left = 0, page0 = 0, page1 = 0;  // of unit v_load
+    int set_end = 0;                               // of ahead
+    const int* table = nullptr;
+    size_t head_off = 0;
     auto look_up = [&]() {
         if (v_load >= u1) return;
-        ahead.seek(p, v_load);
+        if (v_load >= set_end) {
+            ahead.seek(p, v_load);
+            set_end = ahead.begin + ahead.n;
+            table = p.block_table + static_cast<size_t>(ahead.b) * p.max_blocks;
+            head_off = ahead.hkv * block_bytes + lane * 16;
+        }
         key = (v_load - ahead.begin) * KT;
         left = ahead.len - key;
-        const int* entry = p.block_table + static_cast<size_t>(ahead.b) * p.max_blocks + (key >> p.page_shift);
+        const int* entry = table + (key >> p.page_shift);
         page0 = entry[0];
         if (two && left > 16) page1 = entry[1];
     };
@@ -309,8 +329,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 atomicCAS(p.status, 0, FA_ERR_PAGE);
                 page0 = 0;
             }
-            const size_t off = page0 * page_stride + (ahead.hkv * block_bytes + lane * 16) +
-                               static_cast<size_t>((key & ((1 << p.page_shift) - 1)) / kKvqTile) * F::kTileBytes;
+            const uint32_t tile = (key & ((1 << p.page_shift) - 1)) / kKvqTile;
+            const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page0)) * page_stride16 * 16 + head_off +
+                               tile * F::kTileBytes;
             const uint8_t* k0 = p.kpages + off;
             const uint8_t* v0 = p.vpages + off;
             const uint32_t dst = ring_lane + s_load * C::kStageBytes;
@@ -329,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                             atomicCAS(p.status, 0, FA_ERR_PAGE);
                             page1 = 0;
                         }
-                        const size_t to = page1 * page_stride - page0 * page_stride - F::kTileBytes;
+                        const size_t to = (static_cast<int64_t>(page1) - page0) * page_stride16 * 16 - F::kTileBytes;
                         k0 += to;
                         v0 += to;
                     }
@@ -352,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     // ---- the sets of this CTA's run
     const int r = lane >> 2, t = lane & 3;
     float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
+    float* par = reinterpret_cast<float*>(smem + C::kParOff + warp * C::kParBytes);
     int v = u0 + warp, s = 0;
     for (int at = u0; at < u1;) {
         cur.seek(p, at);
@@ -447,10 +469,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             uint8_t* ks = ring + s * C::kStageBytes;
             uint8_t* vs = ks + C::kHalf;
             const int valid = v == last ? cur.len - (v - cur.begin) * KT : KT;
-            const int nb = (valid + 15) / 16;
             if (valid < KT) {
-                // Slots past the last key may hold anything: their V parameters become zero
-                // (a zero probability would not cancel a NaN), their scores -inf below.
+                // Slots past the last key may hold anything, tiles not copied too: their V parameters
+                // become zero (a zero probability would not cancel a NaN), their scores -inf below.
                 for (int i = lane; i < KT * NG; i += 32) {
                     const int key = i / NG;
                     if (key >= valid)
@@ -462,16 +483,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             // ---- scores
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                if (kb >= nb) break;
                 const uint8_t* kt = ks + kb * F::kTileBytes;
                 uint32_t par0[NG], par1[NG];  // keys r and r + 8
                 lds_words(par0, kt + F::kParamOff + r * F::kParamBytes);
                 lds_words(par1, kt + F::kParamOff + (r + 8) * F::kParamBytes);
                 float x1[NT][4], x2[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x1[nt][i] = x2[nt][i] = 0.0f;
                 // x2 = sum over groups of lo sum(q): lo is the A operand, twice in each of thread t's registers
 #pragma unroll
                 for (int zs = 0; zs < C::kZSteps; ++zs) {
@@ -480,7 +496,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     const uint32_t w1 = *reinterpret_cast<const uint32_t*>(kt + at_z + 8 * F::kParamBytes);
                     const uint32_t z0 = __byte_perm(w0, w0, 0x1010), z1 = __byte_perm(w1, w1, 0x1010);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_bf16(x2[nt], z0, z1, z0, z1, qz[nt][zs][0], qz[nt][zs][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (zs == 0) mma_bf16_zero(x2[nt], z0, z1, z0, z1, qz[nt][0][0], qz[nt][0][1]);
+                        else mma_bf16(x2[nt], z0, z1, z0, z1, qz[nt][zs][0], qz[nt][zs][1]);
+                    }
                 }
 #pragma unroll
                 for (int pl = 0; pl < F::kPlanes; ++pl) {
@@ -513,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                         const float s0 = s_of(par0[g]), s1 = s_of(par1[g]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            x1[nt][0] = fmaf(s0, acc[nt][0], x1[nt][0]);
-                            x1[nt][1] = fmaf(s0, acc[nt][1], x1[nt][1]);
-                            x1[nt][2] = fmaf(s1, acc[nt][2], x1[nt][2]);
-                            x1[nt][3] = fmaf(s1, acc[nt][3], x1[nt][3]);
+                            x1[nt][0] = g == 0 ? s0 * acc[nt][0] : fmaf(s0, acc[nt][0], x1[nt][0]);
+                            x1[nt][1] = g == 0 ? s0 * acc[nt][1] : fmaf(s0, acc[nt][1], x1[nt][1]);
+                            x1[nt][2] = g == 0 ? s1 * acc[nt][2] : fmaf(s1, acc[nt][2], x1[nt][2]);
+                            x1[nt][3] = g == 0 ? s1 * acc[nt][3] : fmaf(s1, acc[nt][3], x1[nt][3]);
                         }
                     }
                 }
@@ -531,15 +550,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
                 }
             }
-            // E: every step of the unit's V is below 2^E
+            // V's parameters to fp32, once for the warp: lane l has words NG / 2 l and on of a tile's 16 NG.
+            // E: every step of the unit's V is below 2^E.
             uint32_t top = 0;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                if (kb >= nb) break;
                 uint32_t w[NG / 2];
                 lds_words(w, vs + kb * F::kTileBytes + F::kParamOff + lane * (NG / 2 * 4));
+                const int j = lane / 2;
+                float* to = par + (kb * NG + (lane % 2) * (NG / 2)) * C::kParStride + 4 * (j % 4) + j / 4;
 #pragma unroll
-                for (int i = 0; i < NG / 2; ++i) top = max(top, w[i]);
+                for (int i = 0; i < NG / 2; ++i) {
+                    top = max(top, w[i]);
+                    to[i * C::kParStride] = s_of(w[i]);
+                    to[i * C::kParStride + 16] = lo_of(w[i]);
+                }
             }
             top = __reduce_max_sync(0xffffffffu, top);
             const int e_unit = min(max(static_cast<int>(top >> 23) - 126, -100), 120);
@@ -600,26 +625,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             // ---- output
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                if (kb >= nb) break;
                 const uint8_t* vt = vs + kb * F::kTileBytes;
                 uint32_t wb[NT][NG][2];  // p s of keys (t, t + 4) and (t + 8, t + 12)
-                {
-                    uint32_t par[4][NG];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) lds_words(par[i], vt + F::kParamOff + (4 * i + t) * F::kParamBytes);
+                for (int g = 0; g < NG; ++g) {
+                    const float* from = par + (kb * NG + g) * C::kParStride + 4 * t;
+                    const ulonglong2 sv = *reinterpret_cast<const ulonglong2*>(from);
+                    const ulonglong2 zv = *reinterpret_cast<const ulonglong2*>(from + 16);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float* uu = u[nt] + 4 * kb;
                         const uint64_t u01 = pair(uu[0], uu[1]), u23 = pair(uu[2], uu[3]);
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const float2 w01 = unpair(mul2(u01, pair(s_of(par[0][g]), s_of(par[1][g]))));
-                            const float2 w23 = unpair(mul2(u23, pair(s_of(par[2][g]), s_of(par[3][g]))));
-                            wb[nt][g][0] = pack_f16x2(w01.x, w01.y);
-                            wb[nt][g][1] = pack_f16x2(w23.x, w23.y);
-                            oz[nt][g] = fma2(u01, pair(lo_of(par[0][g]), lo_of(par[1][g])), oz[nt][g]);
-                            oz[nt][g] = fma2(u23, pair(lo_of(par[2][g]), lo_of(par[3][g])), oz[nt][g]);
-                        }
+                        const float2 w01 = unpair(mul2(u01, sv.x)), w23 = unpair(mul2(u23, sv.y));
+                        wb[nt][g][0] = pack_f16x2(w01.x, w01.y);
+                        wb[nt][g][1] = pack_f16x2(w23.x, w23.y);
+                        oz[nt][g] = fma2(u01, zv.x, oz[nt][g]);
+                        oz[nt][g] = fma2(u23, zv.y, oz[nt][g]);
                     }
                 }
 #pragma unroll
@@ -858,6 +879,8 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.cap = max_blocks * page_size;
     // units are counted in int32, a little past the last one too; 16 keys is the shortest
     if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
+    // a page's bytes, in 16s, are counted in uint32
+    if (static_cast<long long>(Hkv) * page_size * kvq_row_bytes(d, bits) / 16 > 0xFFFFFFFFLL) return FA_ERR_INVALID_ARG;
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(H, Hkv, d)) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;
