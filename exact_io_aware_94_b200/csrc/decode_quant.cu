@@ -13,9 +13,15 @@
 // no conversion.  With 0x00f000f0 it gives 16 c 2^-24, and the 1/16 goes into the
 // other operand (scores) or the result (output).  q is scaled by a power of two per
 // head so that its largest value is in [2^14, 2^15): fp16 then holds every bf16 of
-// it exactly down to 2^-29 of that, and to 2^-40 in absolute terms.  The weights
-// p s are rounded to fp16 (11 bits; bf16 has 8) and are below 2^14 by choice of the
-// running reference, so that full precision reaches down to 2^-28 of the greatest.
+// it exactly down to 2^-29 of that, and to 2^-40 in absolute terms.
+//
+// Weights.  u = 2^7 2^(x - m), below 2^15 because the reference m follows the maximum to
+// within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head.  lo
+// and s are scaled by 2^-E, which makes the greatest of a unit less than 1, so fp16 holds
+// their 8 bits down to 2^-17 of that; u s is rounded to fp16 again, u lo is not.  One
+// product of the rounded u with [lo of each group; ones] gives the sums of u lo and of u: the output is
+// divided by the sum of the same rounded weights, so their errors only weigh values
+// against each other and a constant comes out exact.  lse takes the fp32 sum.
 //
 // mma.sync m16n8k16 with the keys (scores) or dimensions (output) as the 16 rows and
 // the heads that share the KV head as the 8 columns: NT = 1 or 2 tiles of 8.  Scores
@@ -54,7 +60,7 @@ constexpr int kThreads = 32 * NC;
 __host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
 constexpr int kMergeDims = 64;      // dimensions merged at once
-constexpr float kRefBits = 6.0f;    // weights are 2^kRefBits times p s / 2^E at the running maximum
+constexpr float kRefBits = 7.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 
 struct DecodeQuantParams {
@@ -87,10 +93,9 @@ struct Cfg {
     static constexpr int S = kRingBudget / (kStageBytes * NC) < 4 ? kRingBudget / (kStageBytes * NC) : 4;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
-    // V's s and lo of a unit in fp32, [tile][group][s, lo][16 keys in score order]; 32 words a group would put
-    // a warp's stores of two groups on the same banks
-    static constexpr int kParStride = 40;
-    static constexpr int kParBytes = kBlocks * F::kGroups * kParStride * 4;
+    // V's s and lo of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], lo [tile][group][key % 4][key / 4]
+    static constexpr int kSBytes = kBlocks * F::kGroups * 32;
+    static constexpr int kParBytes = 2 * kSBytes;
     static constexpr int kZSteps = (F::kGroups + 3) / 4;  // products of lo, 4 groups each
     // shared memory
     static constexpr int kRedBytes = HP * kMergeDims * 4;  // of a warp; its score tile is kept there too
@@ -100,8 +105,10 @@ struct Cfg {
     static constexpr int kZOff = kParOff + NC * kParBytes;           // [warp][head][group]
     static constexpr int kMOff = kZOff + NC * HP * F::kGroups * 4;   // [warp][head] reference
     static constexpr int kLOff = kMOff + NC * HP * 4;                // [warp][head] sum
-    static constexpr int kMiscOff = kLOff + NC * HP * 4;
-    static constexpr int kBytes = kMiscOff + 32 * 4 + 128;
+    static constexpr int kCOff = kLOff + NC * HP * 4;                // [warp][head] sum of the rounded weights
+    static constexpr int kEOff = kCOff + NC * HP * 4;                // [warp] E
+    static constexpr int kMiscOff = kEOff + NC * 4;
+    static constexpr int kBytes = kMiscOff + 32 * 4;
     static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of a CTA");
     static_assert(S >= 2, "a stage is copied while another is read");
     static_assert(HP * kScoreStride * 4 <= kRedBytes, "a warp's scores fit its merge buffer");
@@ -136,25 +143,9 @@ __device__ __forceinline__ void mma_bf16_zero(float (&d)[4], uint32_t a0, uint32
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-// Two fp32 in one register pair, and one instruction for both.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 // fp16 pair, lo in bits 0-15
@@ -222,13 +213,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     using C = Cfg<D, BITS, NT>;
     using F = KvqFormat<D, BITS>;
     constexpr int KT = C::KT, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may be set up while this one runs
     float* red_all = reinterpret_cast<float*>(smem + C::kRedOff);
     float* red_z = reinterpret_cast<float*>(smem + C::kZOff);
     float* red_m = reinterpret_cast<float*>(smem + C::kMOff);
     float* red_l = reinterpret_cast<float*>(smem + C::kLOff);
+    float* red_c = reinterpret_cast<float*>(smem + C::kCOff);
+    int* red_e = reinterpret_cast<int*>(smem + C::kEOff);
     int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] exit, [1..4] first set, [8..] scan
 
     // ---- plan: the number of units and the set of this CTA's first one
@@ -373,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     // ---- the sets of this CTA's run
     const int r = lane >> 2, t = lane & 3;
     float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
-    float* par = reinterpret_cast<float*>(smem + C::kParOff + warp * C::kParBytes);
+    uint8_t* par = smem + C::kParOff + warp * C::kParBytes;
     int v = u0 + warp, s = 0;
     for (int at = u0; at < u1;) {
         cur.seek(p, at);
@@ -383,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         const size_t head0 = static_cast<size_t>(cur.b) * p.H + cur.hkv * group + h_in;
 
         float o[NT][D / 16][4];
-        uint64_t oz[NT][NG];  // sums of p lo over the thread's even and odd keys
+        float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u lo of group r, sums of u
         float m[NT], l[NT];
         int E = -1000;
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
@@ -394,13 +387,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = -INFINITY;
             l[nt] = 0.0f;
+            oc[nt][0] = oc[nt][1] = oc[nt][2] = oc[nt][3] = 0.0f;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
             uint4 raw[NG];
             const int h = nt * 8 + r;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                oz[nt][g] = 0;
                 raw[g] = h < G ? *reinterpret_cast<const uint4*>(p.q + (head0 + h) * D + g * kKvqGroup + t * 8)
                                : make_uint4(0, 0, 0, 0);
             }
@@ -550,24 +543,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
                 }
             }
-            // V's parameters to fp32, once for the warp: lane l has words NG / 2 l and on of a tile's 16 NG.
-            // E: every step of the unit's V is below 2^E.
-            uint32_t top = 0;
+            // V's parameters: lane l has words NG / 2 l and on of a tile's 16 NG.  All are below 2^E.
+            uint32_t pw[NB][NG / 2], top = 0;
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
-                uint32_t w[NG / 2];
-                lds_words(w, vs + kb * F::kTileBytes + F::kParamOff + lane * (NG / 2 * 4));
-                const int j = lane / 2;
-                float* to = par + (kb * NG + (lane % 2) * (NG / 2)) * C::kParStride + 4 * (j % 4) + j / 4;
+                lds_words(pw[kb], vs + kb * F::kTileBytes + F::kParamOff + lane * (NG / 2 * 4));
 #pragma unroll
-                for (int i = 0; i < NG / 2; ++i) {
-                    top = max(top, w[i]);
-                    to[i * C::kParStride] = s_of(w[i]);
-                    to[i * C::kParStride + 16] = lo_of(w[i]);
-                }
+                for (int i = 0; i < NG / 2; ++i) top = max(top, max(pw[kb][i], (pw[kb][i] << 16) & 0x7FFF0000u));
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            const int e_unit = min(max(static_cast<int>(top >> 23) - 126, -100), 120);
+            if (top >= 0x7F800000u) {  // a group stands for NaN: E goes by the others
+                top = 0;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int i = 0; i < NG / 2; ++i) {
+                        const uint32_t hi = pw[kb][i] & 0x7FFF0000u, lo = (pw[kb][i] << 16) & 0x7FFF0000u;
+                        top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
+                    }
+                top = __reduce_max_sync(0xffffffffu, top);
+            }
+            const int e_unit = min(max(static_cast<int>(top >> 23) - 126, -100), 126);
             __syncwarp();
             // ---- softmax: thread (head r, t) takes keys t, t + 4, t + 8, t + 12 of each block
             float u[NT][4 * NB];
@@ -595,52 +591,78 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             }
             if (__any_sync(0xffffffffu, grow)) {
                 const int e_new = max(E, e_unit);
+                const float fall = ex2_approx(static_cast<float>(E - e_new));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float alpha = m[nt] == -INFINITY ? 0.0f : ex2_approx((m[nt] - m_new[nt]) + static_cast<float>(E - e_new));
+                    const float alpha = m[nt] == -INFINITY ? 0.0f : ex2_approx(m[nt] - m_new[nt]);
                     m[nt] = m_new[nt];
                     l[nt] *= alpha;
                     const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) oz[nt][g] = mul2(oz[nt][g], pair(alpha, alpha));
+                    oc[nt][0] *= al0 * fall;
+                    oc[nt][1] *= al1 * fall;
+                    oc[nt][2] *= al0;
+                    oc[nt][3] *= al1;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        o[nt][j][0] *= al0;
-                        o[nt][j][1] *= al1;
-                        o[nt][j][2] *= al0;
-                        o[nt][j][3] *= al1;
+                        o[nt][j][0] *= al0 * fall;
+                        o[nt][j][1] *= al1 * fall;
+                        o[nt][j][2] *= al0 * fall;
+                        o[nt][j][3] *= al1 * fall;
                     }
                 }
                 E = e_new;
             }
+            {
+                // lane l: key l / 2's parameters of groups NG / 2 (l % 2) and on, into the order the products want
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
+                const int k4 = (lane / 2) % 4, ki = lane / 8, g0 = (lane % 2) * (NG / 2);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float bias = kRefBits - static_cast<float>(E) - (m[nt] == -INFINITY ? 0.0f : m[nt]);
+                for (int kb = 0; kb < NB; ++kb) {
+                    uint8_t* s_to = par + ((kb * 4 + k4) * NG + g0) * 8 + ki * 2;
+                    uint8_t* z_to = par + C::kSBytes + (kb * NG + g0) * 32 + k4 * 8 + ki * 2;
 #pragma unroll
-                for (int i = 0; i < 4 * NB; ++i) {
-                    u[nt][i] = ex2_approx(u[nt][i] + bias);
-                    l[nt] += u[nt][i];
+                    for (int i = 0; i < NG / 2; ++i) {
+                        const uint32_t sz = pack_f16x2(s_of(pw[kb][i]) * down, lo_of(pw[kb][i]) * down);
+                        *reinterpret_cast<uint16_t*>(s_to + i * 8) = static_cast<uint16_t>(sz);
+                        *reinterpret_cast<uint16_t*>(z_to + i * 32) = static_cast<uint16_t>(sz >> 16);
+                    }
                 }
             }
+            uint32_t uh[NT][NB][2];  // the weights in fp16: keys (t, t + 4) and (t + 8, t + 12)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float bias = kRefBits - (m[nt] == -INFINITY ? 0.0f : m[nt]);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) {
+                    float* x = u[nt] + 4 * kb;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = ex2_approx(x[i] + bias);
+                        l[nt] += x[i];
+                    }
+                    uh[nt][kb][0] = pack_f16x2(x[0], x[1]);
+                    uh[nt][kb][1] = pack_f16x2(x[2], x[3]);
+                }
+            }
+            __syncwarp();
             // ---- output
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 const uint8_t* vt = vs + kb * F::kTileBytes;
-                uint32_t wb[NT][NG][2];  // p s of keys (t, t + 4) and (t + 8, t + 12)
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float* from = par + (kb * NG + g) * C::kParStride + 4 * t;
-                    const ulonglong2 sv = *reinterpret_cast<const ulonglong2*>(from);
-                    const ulonglong2 zv = *reinterpret_cast<const ulonglong2*>(from + 16);
+                uint32_t wb[NT][NG][2];  // u s of keys (t, t + 4) and (t + 8, t + 12)
+                {
+                    uint32_t sw[2 * NG], zw[2];
+                    lds_words(sw, par + (kb * 4 + t) * NG * 8);
+                    lds_words(zw, par + C::kSBytes + (kb * NG + r % NG) * 32 + t * 8);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float* uu = u[nt] + 4 * kb;
-                        const uint64_t u01 = pair(uu[0], uu[1]), u23 = pair(uu[2], uu[3]);
-                        const float2 w01 = unpair(mul2(u01, sv.x)), w23 = unpair(mul2(u23, sv.y));
-                        wb[nt][g][0] = pack_f16x2(w01.x, w01.y);
-                        wb[nt][g][1] = pack_f16x2(w23.x, w23.y);
-                        oz[nt][g] = fma2(u01, zv.x, oz[nt][g]);
-                        oz[nt][g] = fma2(u23, zv.y, oz[nt][g]);
+                        constexpr uint32_t kOnes = 0x3C003C00u;
+                        mma_f16(oc[nt], zw[0], kOnes, zw[1], kOnes, uh[nt][kb][0], uh[nt][kb][1]);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            wb[nt][g][0] = mul_f16x2(uh[nt][kb][0], sw[2 * g]);
+                            wb[nt][g][1] = mul_f16x2(uh[nt][kb][1], sw[2 * g + 1]);
+                        }
                     }
                 }
 #pragma unroll
@@ -687,20 +709,18 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-            const int at_h = warp * HP + nt * 8 + r;
             if (t == 0) {
-                red_m[at_h] = m[nt] == -INFINITY ? -INFINITY : m[nt] + static_cast<float>(E);
-                red_l[at_h] = l[nt];
+                red_m[warp * HP + nt * 8 + r] = m[nt];
+                red_l[warp * HP + nt * 8 + r] = l[nt];
             }
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float2 two = unpair(oz[nt][g]);
-                float z = two.x + two.y;
-                z += __shfl_xor_sync(0xffffffffu, z, 1);
-                z += __shfl_xor_sync(0xffffffffu, z, 2);
-                if (t == 0) red_z[at_h * NG + g] = z;
+            for (int c = 0; c < 2; ++c) {
+                const int at_h = warp * HP + nt * 8 + 2 * t + c;
+                if (r < NG) red_z[at_h * NG + r] = oc[nt][c];
+                if (r == 0) red_c[at_h] = oc[nt][2 + c];
             }
         }
+        if (lane == 0) red_e[warp] = E;
         const bool whole = at == cur.begin && end == cur.begin + cur.n;
         const int slot = 2 * cta + (at > cur.begin ? 0 : 1);
         constexpr float kUp = 16777216.0f;  // 2^24 of the codes
@@ -724,18 +744,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             for (int e = tid; e < G * kMergeDims; e += kThreads) {
                 const int h = e / kMergeDims, c = e % kMergeDims, d = md * kMergeDims + c;
                 float M = -INFINITY;
+                int Em = -100;
 #pragma unroll
-                for (int w = 0; w < NC; ++w) M = fmaxf(M, red_m[w * HP + h]);
-                float L = 0.0f, O = 0.0f;
+                for (int w = 0; w < NC; ++w) {
+                    M = fmaxf(M, red_m[w * HP + h]);
+                    Em = max(Em, red_e[w]);
+                }
+                float L = 0.0f, W = 0.0f, O = 0.0f;
 #pragma unroll
                 for (int w = 0; w < NC; ++w) {
                     const float mw = red_m[w * HP + h];
                     // no finite score: nothing seen, or only NaN and -inf (then l and O say so)
                     const float wt = mw == M ? 1.0f : ex2_approx(mw - M);
                     L = fmaf(wt, red_l[w * HP + h], L);
-                    O = fmaf(wt, red_all[(w * HP + h) * kMergeDims + c] + red_z[(w * HP + h) * NG + d / kKvqGroup], O);
+                    W = fmaf(wt, red_c[w * HP + h], W);
+                    O = fmaf(wt * ex2_approx(static_cast<float>(red_e[w] - Em)),
+                             red_all[(w * HP + h) * kMergeDims + c] + red_z[(w * HP + h) * NG + d / kKvqGroup], O);
                 }
-                O /= L;
+                O = O / W * __uint_as_float(static_cast<uint32_t>(127 + Em) << 23);
                 if (whole) {
                     if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[(head0 + h) * D + d] = O;
                     else static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(O);
@@ -761,12 +787,13 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
     __shared__ float s_w[HP][max_ctas(D, NT)];  // of part c0 + i, normalised
     __shared__ float s_o[kCombineThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (*static_cast<volatile const int*>(p.status) == FA_ERR_TIMEOUT) return;
-    const int2 plan = *p.plan;
     const int i = blockIdx.x + 1;
-    if (i >= plan.y) return;
-    const long long U = plan.x, n_cta = plan.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel has ended and its writes are visible
+    const int status = *static_cast<volatile const int*>(p.status);
+    const int2 plan = *p.plan;
     const int4 set = p.first[i];  // sequence, set, first unit, units
+    if (status == FA_ERR_TIMEOUT || i >= plan.y) return;
+    const long long U = plan.x, n_cta = plan.y;
     if (set.z == static_cast<int>(U * i / n_cta)) return;  // starts with the CTA
     const int c0 = static_cast<int>(((set.z + 1LL) * n_cta - 1) / U);
     const int P = static_cast<int>((static_cast<long long>(set.z + set.w) * n_cta - 1) / U) - c0 + 1;
@@ -779,6 +806,36 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
     if (e0 >= e1) return;
     // part i is the last one CTA c0 wrote (slot 2 c0 + 1), or the first one of a later CTA
     auto slot = [&](int c) { return static_cast<size_t>(2 * (c0 + c) + (c == 0)) * HP; };
+    auto store = [&](int e, float x) {
+        const size_t at = (head0 + e / D) * D + e % D;
+        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[at] = x;
+        else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
+    };
+    constexpr int kFew = 6;
+    if (P <= kFew) {  // a thread an output, all its loads at once
+        for (int e = e0 + tid; e < e1; e += kCombineThreads) {
+            const int h = e / D, d = e % D;
+            float x[kFew], y[kFew], M = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < kFew; ++c) {
+                x[c] = c < P ? p.part_lse[slot(c) + h] : -INFINITY;
+                y[c] = c < P ? p.part_o[(slot(c) + h) * D + d] : 0.0f;
+            }
+#pragma unroll
+            for (int c = 0; c < kFew; ++c) M = fmaxf(M, x[c]);
+            float L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kFew; ++c) {
+                if (c >= P) break;
+                const float w = x[c] == M ? 1.0f : ex2_approx(x[c] - M);
+                L += w;
+                O = fmaf(w, y[c], O);
+            }
+            store(e, O / L);
+            if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+        }
+        return;
+    }
     for (int h = e0 / D + warp; h <= (e1 - 1) / D; h += kCombineThreads / 32) {
         float M = -INFINITY;
         for (int c = lane; c < P; c += 32) {
@@ -799,11 +856,6 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
         if (lane == 0 && h * D >= e0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
-    auto store = [&](int e, float x) {
-        const size_t at = (head0 + e / D) * D + e % D;
-        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[at] = x;
-        else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
-    };
     // W columns of outputs, kCombineThreads / W threads each
     int W = kCombineThreads;
     while (W > 4 && W / 2 >= share) W /= 2;
@@ -835,8 +887,17 @@ cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream)
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
     const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
     fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
-    if (grid > 1) fa_decode_quant_combine<D, NT><<<grid - 1, kCombineThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid - 1);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_decode_quant_combine<D, NT>, p);
 }
 
 // 8-head tiles of a set: two (O takes NT D / 4 registers a thread) only where a second

@@ -106,8 +106,13 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
 
     Tolerances.  A score is a sum over groups of s (q . c) + lo sum(q): with X the sum of its terms' magnitudes (in
     nats) and at most 14 fp32 roundings on the way (two accumulations a group that may truncate, d / 32 + 2 fused
-    sums), it is off by less than 2^-20 X, and the exponential by 2^-22 more.  The weight p s of a code is rounded to
-    fp16 once: 2^-11 of sum(p s c) / sum(p).  lse adds its own fp32 rounding."""
+    sums), it is off by less than 2^-20 X, and the exponential by 2^-22 more.  lse adds its own fp32 rounding.
+    A probability's weight u is rounded to fp16 for the output, which is divided by the sum of the rounded weights:
+    with u (1 + e), |e| <= 2^-11, the output moves by sum(p e (v - o)) at first order.  The product u s that weighs
+    a code is rounded to fp16 again: 2^-11 of sum(p s c).  fp16 steps end at 2^-24: as the greatest u is at least
+    2^7 and lo and s are scaled by the power of two above the greatest, M, each of n keys adds at most
+    2^-25 / 2^7 (|v - o| + 2 M c), and the rounding of s or lo itself 2^-25 * 2 M (c + 1) on average over the keys.
+    The factor 1 + 2^-8 covers the products of these errors."""
     B, H, d = q.shape
     Hkv = kpool.shape[1]
     G = H // Hkv
@@ -131,6 +136,10 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
                 ex = 2.0 ** -20 * X.max() + 2.0 ** -21
                 v = (vlo + vs * vc)[:, g]
                 o[b, h] = p @ v
-                tol_o[b, h] = 2.0 ** -11 * (p @ (vs * vc)[:, g]) + 2 * ex * (p @ (np.abs(vlo) + vs * vc)[:, g])
+                far, M = np.abs(v - o[b, h]), np.nanmax([np.nanmax(np.abs(vlo[:, g])), np.nanmax(vs[:, g])])
+                top = 2 ** bits - 1
+                tol_o[b, h] = (1 + 2.0 ** -8) * (
+                    2.0 ** -11 * (p @ far + p @ (vs * vc)[:, g]) + 2 * ex * (p @ (np.abs(vlo) + vs * vc)[:, g])
+                    + n * 2.0 ** -32 * (far.max(0) + 2 * M * top) + 2.0 ** -24 * M * (top + 1))
                 tol_l[b, h] = ex + 2.0 ** -22 * abs(lse[b, h])
     return o, lse, tol_o, tol_l
