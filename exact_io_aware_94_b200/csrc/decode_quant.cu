@@ -31,14 +31,15 @@
 // which is what the cache's order of dimensions inside a token is for.
 //
 // Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  The units
-// of the whole batch, in that order, are cut into equal runs, one a CTA; warp w of a
-// CTA takes units u0 + w, u0 + w + 4, ... of its run.  Each of the four warps copies its own
-// units into a ring of S stages of its own with 16-byte asynchronous copies (a 16-token
-// tile of K or of V is one run of bytes), so no warp waits for another in the loop.
-// Where the run crosses into another (sequence, head set), the warps merge their
-// statistics and write the output, or, if the set's keys are shared with another CTA, a
-// partial one that fa_decode_quant_combine merges.  An SM holds several CTAs, so that one
-// computes while another starts, merges or ends.
+// of the whole batch, in that order, are cut into equal runs, one a CTA, and a CTA's run
+// into equal runs for its four warps.  A warp copies its units into a ring of S
+// stages of its own with 16-byte asynchronous copies (a 16-token tile of K or of V is
+// one run of bytes) and waits for no other warp: a set that lies in its run whole it
+// writes out itself.  A set that is cut at a warp's border leaves a part (normalised output and log-sum-exp) on
+// either side; the CTA merges its parts once, at its end, and writes those of a set that
+// is cut at its own border for fa_decode_quant_combine.  (Dealing a CTA's units to its warps in turn takes a
+// merge of the warps for every set: batches of short sequences then had CTAs that took 1.5
+// times as long as the rest.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -59,7 +60,6 @@ constexpr int kThreads = 32 * NC;
 // CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone takes nt d / 4.
 __host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
-constexpr int kMergeDims = 64;      // dimensions merged at once
 constexpr float kRefBits = 7.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 
@@ -73,6 +73,7 @@ struct DecodeQuantParams {
     float* lse;
     int* status;
     float* part_o;    // [2 * CTAs][8 NT][D], normalised
+    float* part_w;    // [CTAs][warps][8 NT][D]: the part of the set that a warp's run starts inside of
     float* part_lse;  // [2 * CTAs][8 NT], base 2
     int4* first;      // [CTAs]: (sequence, head set, first unit, units) of the set that holds a CTA's first unit
     int2* plan;       // units of the batch, CTAs that share them
@@ -97,21 +98,19 @@ struct Cfg {
     static constexpr int kSBytes = kBlocks * F::kGroups * 32;
     static constexpr int kParBytes = 2 * kSBytes;
     static constexpr int kZSteps = (F::kGroups + 3) / 4;  // products of lo, 4 groups each
-    // shared memory
-    static constexpr int kRedBytes = HP * kMergeDims * 4;  // of a warp; its score tile is kept there too
+    // shared memory; a warp's last part is kept in its ring
+    static constexpr int kScoreBytes = HP * kScoreStride * 4;
+    static constexpr int kRingBytes = S * kStageBytes;  // of a warp
     static constexpr int kRingOff = 0;
-    static constexpr int kRedOff = kRingOff + NC * S * kStageBytes;
-    static constexpr int kParOff = kRedOff + NC * kRedBytes;
-    static constexpr int kZOff = kParOff + NC * kParBytes;           // [warp][head][group]
-    static constexpr int kMOff = kZOff + NC * HP * F::kGroups * 4;   // [warp][head] reference
-    static constexpr int kLOff = kMOff + NC * HP * 4;                // [warp][head] sum
-    static constexpr int kCOff = kLOff + NC * HP * 4;                // [warp][head] sum of the rounded weights
-    static constexpr int kEOff = kCOff + NC * HP * 4;                // [warp] E
-    static constexpr int kMiscOff = kEOff + NC * 4;
+    static constexpr int kScoreOff = kRingOff + NC * kRingBytes;
+    static constexpr int kParOff = kScoreOff + NC * kScoreBytes;
+    static constexpr int kMetaOff = kParOff + NC * kParBytes;          // [warp][first, last part] of Part
+    static constexpr int kLseOff = kMetaOff + NC * 2 * 32;             // [warp][first, last part][head], base 2
+    static constexpr int kMiscOff = kLseOff + NC * 2 * HP * 4;
     static constexpr int kBytes = kMiscOff + 32 * 4;
     static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of a CTA");
     static_assert(S >= 2, "a stage is copied while another is read");
-    static_assert(HP * kScoreStride * 4 <= kRedBytes, "a warp's scores fit its merge buffer");
+    static_assert(HP * D * 4 <= kRingBytes, "a part fits a warp's ring");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -208,6 +207,13 @@ __device__ __forceinline__ void copy_wait() {  // all but the last N groups of t
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// What a warp leaves of a set that is cut at the border of its run.
+struct Part {
+    int kind;  // 0: none; first part: 1 ends in the run, 2 goes on after it; last part: 1
+    int b, hkv, set;
+    int pad[4];
+};
+
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
     using C = Cfg<D, BITS, NT>;
@@ -216,12 +222,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may be set up while this one runs
-    float* red_all = reinterpret_cast<float*>(smem + C::kRedOff);
-    float* red_z = reinterpret_cast<float*>(smem + C::kZOff);
-    float* red_m = reinterpret_cast<float*>(smem + C::kMOff);
-    float* red_l = reinterpret_cast<float*>(smem + C::kLOff);
-    float* red_c = reinterpret_cast<float*>(smem + C::kCOff);
-    int* red_e = reinterpret_cast<int*>(smem + C::kEOff);
+    Part* parts = reinterpret_cast<Part*>(smem + C::kMetaOff);
+    float* part_lse = reinterpret_cast<float*>(smem + C::kLseOff);
     int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] exit, [1..4] first set, [8..] scan
 
     // ---- plan: the number of units and the set of this CTA's first one
@@ -290,20 +292,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     Cursor<KT> cur{misc[1], misc[2] / p.sets, misc[2] % p.sets, misc[3], units_of<KT>(misc[4]), misc[4]};
     const int group = p.H / p.Hkv;
 
-    // ---- copies: this warp's units u0 + warp + NC i, stage i % S
-    uint8_t* ring = smem + C::kRingOff + warp * (S * C::kStageBytes);
+    // ---- copies: this warp's units [w0, w1), unit w0 + i in stage i % S
+    uint8_t* ring = smem + C::kRingOff + warp * C::kRingBytes;
     const uint32_t ring_lane = smem_u32(ring) + lane * 16;
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
     const uint32_t page_stride16 = static_cast<uint32_t>(block_bytes * p.Hkv / 16);
     const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
     Cursor<KT> ahead = cur;
-    int v_load = u0 + warp, s_load = 0;
+    const int w0 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * warp / NC);
+    const int w1 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * (warp + 1) / NC);
+    int v_load = w0, s_load = 0;
     int key = 0, left = 0, page0 = 0, page1 = 0;  // of unit v_load
     int set_end = 0;                               // of ahead
     const int* table = nullptr;
     size_t head_off = 0;
     auto look_up = [&]() {
-        if (v_load >= u1) return;
+        if (v_load >= w1) return;
         if (v_load >= set_end) {
             ahead.seek(p, v_load);
             set_end = ahead.begin + ahead.n;
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         if (two && left > 16) page1 = entry[1];
     };
     auto issue = [&]() {
-        if (v_load < u1) {
+        if (v_load < w1) {
             if (static_cast<unsigned>(page0) >= static_cast<unsigned>(p.num_pages)) {
                 atomicCAS(p.status, 0, FA_ERR_PAGE);
                 page0 = 0;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     }
                 }
             }
-            v_load += NC;
+            ++v_load;
             s_load = s_load + 1 == S ? 0 : s_load + 1;
             look_up();
         }
@@ -363,14 +367,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue();
 
-    // ---- the sets of this CTA's run
+    // ---- the sets of this warp's run
+    if (lane < 2) parts[2 * warp + lane].kind = 0;
+    __syncwarp();
     const int r = lane >> 2, t = lane & 3;
-    float* sc = red_all + warp * (C::kRedBytes / 4);  // [head][KT + 4]: this warp's scores
+    float* sc = reinterpret_cast<float*>(smem + C::kScoreOff + warp * C::kScoreBytes);  // [head][key]: scores
     uint8_t* par = smem + C::kParOff + warp * C::kParBytes;
-    int v = u0 + warp, s = 0;
-    for (int at = u0; at < u1;) {
+    int s = 0;
+    for (int at = w0; at < w1;) {
         cur.seek(p, at);
-        const int end = min(u1, cur.begin + cur.n);
+        const int end = min(w1, cur.begin + cur.n);
         const int h_in = cur.set * HP;
         const int G = min(HP, group - h_in);  // heads of the set
         const size_t head0 = static_cast<size_t>(cur.b) * p.H + cur.hkv * group + h_in;
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         }
 
         const int last = cur.begin + cur.n - 1;  // the only unit that may be short
-        for (; v < end; v += NC) {
+        for (int v = at; v < end; ++v) {
             issue();
             copy_wait<S - 1>();
             __syncwarp();
@@ -704,77 +710,114 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             s = s + 1 == S ? 0 : s + 1;
         }
 
-        // ---- merge the warps: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of heads 2 t, 2 t + 1
+        // ---- the set's output, or this warp's part of it: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of
+        // heads 2 t, 2 t + 1
+        const bool before = at > cur.begin, after = end < cur.begin + cur.n;
+        const bool whole = !before && !after;
+        float* part = before ? p.part_w + (static_cast<size_t>(cta) * NC + warp) * HP * D : reinterpret_cast<float*>(ring);
+        __syncwarp();  // the ring has been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-            if (t == 0) {
-                red_m[warp * HP + nt * 8 + r] = m[nt];
-                red_l[warp * HP + nt * 8 + r] = l[nt];
+            // no finite score (only NaN and -inf): l says so
+            const float lse = (m[nt] == -INFINITY ? 0.0f : m[nt]) - kRefBits + log2f(l[nt]);
+            const int h = nt * 8 + r;
+            if (t == 0 && h < G) {
+                if (whole) p.lse[head0 + h] = lse * 0.6931471805599453f;
+                else part_lse[(2 * warp + (before ? 0 : 1)) * HP + h] = lse;
             }
+            constexpr float kUp = 16777216.0f;  // 2^24 of the codes
+            constexpr float kUp1 = BITS == 4 ? kUp / 16.0f : kUp;
+            const float scale_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int at_h = warp * HP + nt * 8 + 2 * t + c;
-                if (r < NG) red_z[at_h * NG + r] = oc[nt][c];
-                if (r == 0) red_c[at_h] = oc[nt][2 + c];
-            }
-        }
-        if (lane == 0) red_e[warp] = E;
-        const bool whole = at == cur.begin && end == cur.begin + cur.n;
-        const int slot = 2 * cta + (at > cur.begin ? 0 : 1);
-        constexpr float kUp = 16777216.0f;  // 2^24 of the codes
-        constexpr float kUp1 = BITS == 4 ? kUp / 16.0f : kUp;
+                const int hc = nt * 8 + 2 * t + c;
+                const float inv = oc[nt][2 + c] == 0.0f ? 0.0f : 1.0f / oc[nt][2 + c];  // 0: every score is -inf
 #pragma unroll
-        for (int md = 0; md < D / kMergeDims; ++md) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int gi = 0; gi < kMergeDims / kKvqGroup; ++gi) {
-                    const int g = md * (kMergeDims / kKvqGroup) + gi;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float* o0 = o[nt][2 * g];
-                        const float* o1 = o[nt][2 * g + 1];
-                        *reinterpret_cast<float4*>(sc + (nt * 8 + 2 * t + c) * kMergeDims + gi * kKvqGroup + 4 * r) =
-                            make_float4(o0[c] * kUp, o0[c + 2] * kUp1, o1[c] * kUp, o1[c + 2] * kUp1);
+                for (int g = 0; g < NG; ++g) {
+                    const float z = __shfl_sync(0xffffffffu, oc[nt][c], 4 * g + t);
+                    const float* o0 = o[nt][2 * g];
+                    const float* o1 = o[nt][2 * g + 1];
+                    float4 x = make_float4(fmaf(o0[c], kUp, z) * inv * scale_e, fmaf(o0[c + 2], kUp1, z) * inv * scale_e,
+                                           fmaf(o1[c], kUp, z) * inv * scale_e, fmaf(o1[c + 2], kUp1, z) * inv * scale_e);
+                    const int d = g * kKvqGroup + 4 * r;
+                    if (hc >= G) continue;
+                    if (!whole) {
+                        *reinterpret_cast<float4*>(part + hc * D + d) = x;
+                    } else if (p.o_dtype == FA_DT_F32) {
+                        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + hc) * D + d) = x;
+                    } else {
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + hc) * D + d) =
+                            make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
                     }
                 }
-            __syncthreads();
-            for (int e = tid; e < G * kMergeDims; e += kThreads) {
-                const int h = e / kMergeDims, c = e % kMergeDims, d = md * kMergeDims + c;
-                float M = -INFINITY;
-                int Em = -100;
-#pragma unroll
-                for (int w = 0; w < NC; ++w) {
-                    M = fmaxf(M, red_m[w * HP + h]);
-                    Em = max(Em, red_e[w]);
-                }
-                float L = 0.0f, W = 0.0f, O = 0.0f;
-#pragma unroll
-                for (int w = 0; w < NC; ++w) {
-                    const float mw = red_m[w * HP + h];
-                    // no finite score: nothing seen, or only NaN and -inf (then l and O say so)
-                    const float wt = mw == M ? 1.0f : ex2_approx(mw - M);
-                    L = fmaf(wt, red_l[w * HP + h], L);
-                    W = fmaf(wt, red_c[w * HP + h], W);
-                    O = fmaf(wt * ex2_approx(static_cast<float>(red_e[w] - Em)),
-                             red_all[(w * HP + h) * kMergeDims + c] + red_z[(w * HP + h) * NG + d / kKvqGroup], O);
-                }
-                O = O / W * __uint_as_float(static_cast<uint32_t>(127 + Em) << 23);
-                if (whole) {
-                    if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[(head0 + h) * D + d] = O;
-                    else static_cast<__nv_bfloat16*>(p.o)[(head0 + h) * D + d] = __float2bfloat16_rn(O);
-                    if (d == 0) p.lse[head0 + h] = (M - kRefBits + log2f(L)) * 0.6931471805599453f;
-                } else {
-                    p.part_o[(static_cast<size_t>(slot) * HP + h) * D + d] = O;
-                    if (d == 0) p.part_lse[slot * HP + h] = M - kRefBits + log2f(L);
-                }
             }
-            __syncthreads();
         }
+        if (!whole && lane == 0) parts[2 * warp + (before ? 0 : 1)] = Part{before && after ? 2 : 1, cur.b, cur.hkv, cur.set, {}};
         at = end;
     }
+
+    // ---- the CTA's parts: those of one set are neighbours in the order first, last of warp 0, first, last of warp 1, ...
+    __syncthreads();
+    const float* from[NC];
+    const float* from_lse[NC];
+    int n_from = 0;
+    bool before = false;
+    Part of{};
+    auto merge = [&](bool after) {
+        const int h_in = of.set * HP, G = min(HP, group - h_in);
+        const size_t head0 = static_cast<size_t>(of.b) * p.H + of.hkv * group + h_in;
+        const bool whole = !before && !after;
+        const size_t slot = static_cast<size_t>(2 * cta + (before ? 0 : 1)) * HP;
+        for (int e = tid; e < G * (D / 4); e += kThreads) {
+            const int h = e / (D / 4), d = e % (D / 4) * 4;
+            float M = -INFINITY, L = 0.0f;
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (i < n_from) M = fmaxf(M, from_lse[i][h]);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if (i >= n_from) break;
+                const float x = from_lse[i][h];
+                const float w = x == M ? 1.0f : ex2_approx(x - M);
+                const float4 y = *reinterpret_cast<const float4*>(from[i] + h * D + d);
+                L += w;
+                O.x = fmaf(w, y.x, O.x), O.y = fmaf(w, y.y, O.y), O.z = fmaf(w, y.z, O.z), O.w = fmaf(w, y.w, O.w);
+            }
+            const float inv = 1.0f / L;
+            O.x *= inv, O.y *= inv, O.z *= inv, O.w *= inv;
+            if (!whole) {
+                *reinterpret_cast<float4*>(p.part_o + (slot + h) * D + d) = O;
+                if (d == 0) p.part_lse[slot + h] = M + log2f(L);
+            } else {
+                if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + h) * D + d) = O;
+                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
+                    make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
+                if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+            }
+        }
+        n_from = 0;
+        before = false;
+    };
+#pragma unroll
+    for (int w = 0; w < NC; ++w) {
+        const Part first = parts[2 * w], last = parts[2 * w + 1];
+        if (first.kind) {
+            if (n_from == 0) before = true;  // only warp 0's: the set starts before the CTA
+            of = first;
+            from[n_from] = p.part_w + (static_cast<size_t>(cta) * NC + w) * HP * D;
+            from_lse[n_from++] = part_lse + 2 * w * HP;
+            if (first.kind == 1) merge(false);
+        }
+        if (last.kind) {
+            of = last;
+            from[n_from] = reinterpret_cast<const float*>(smem + C::kRingOff + w * C::kRingBytes);
+            from_lse[n_from++] = part_lse + (2 * w + 1) * HP;
+        }
+    }
+    if (n_from) merge(true);
 }
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
@@ -906,9 +949,10 @@ int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 size_t part_bytes(int d, int nt) { return up256(static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * (d + 1) * sizeof(float)); }
+size_t warp_part_bytes(int d, int nt) { return up256(static_cast<size_t>(max_ctas(d, nt)) * NC * 8 * nt * d * sizeof(float)); }
 size_t workspace_bytes_of(int H, int Hkv, int d) {
     const int nt = tiles_of(H / Hkv, d);
-    return part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)) + 256;
+    return part_bytes(d, nt) + warp_part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)) + 256;
 }
 
 }  // namespace
@@ -958,8 +1002,11 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_lse = p.part_o + static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * d;
-    p.first = reinterpret_cast<int4*>(ws + part_bytes(d, nt));
-    p.plan = reinterpret_cast<int2*>(ws + part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)));
+    ws += part_bytes(d, nt);
+    p.part_w = reinterpret_cast<float*>(ws);
+    ws += warp_part_bytes(d, nt);
+    p.first = reinterpret_cast<int4*>(ws);
+    p.plan = reinterpret_cast<int2*>(ws + up256(max_ctas(d, nt) * sizeof(int4)));
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
