@@ -62,6 +62,7 @@ __host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 
 __host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
 constexpr float kRefBits = 7.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
+constexpr float kNoMax = -1e30f;    // the maximum of no score: finite, so that no difference is NaN
 
 struct DecodeQuantParams {
     const __nv_bfloat16* q;  // [B, H, D]
@@ -96,6 +97,8 @@ struct Cfg {
     static constexpr int kScoreStride = KT + 4;
     // V's s and lo of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], lo [tile][group][key % 4][key / 4]
     static constexpr int kSBytes = kBlocks * F::kGroups * 32;
+    static constexpr int kPairs = kBlocks * F::kGroups / 4;  // pairs of keys of a group that a thread converts
+    static_assert(kPairs > 0, "a unit has a pair for every thread");
     static constexpr int kParBytes = 2 * kSBytes;
     static constexpr int kZSteps = (F::kGroups + 3) / 4;  // products of lo, 4 groups each
     // shared memory; a warp's last part is kept in its ring
@@ -320,41 +323,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         page0 = entry[0];
         if (two && left > 16) page1 = entry[1];
     };
+    auto page_in = [&](int page) {
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
+        atomicCAS(p.status, 0, FA_ERR_PAGE);
+        return 0;
+    };
     auto issue = [&]() {
         if (v_load < w1) {
-            if (static_cast<unsigned>(page0) >= static_cast<unsigned>(p.num_pages)) {
-                atomicCAS(p.status, 0, FA_ERR_PAGE);
-                page0 = 0;
-            }
             const uint32_t tile = (key & ((1 << p.page_shift) - 1)) / kKvqTile;
-            const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page0)) * page_stride16 * 16 + head_off +
+            const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page0))) * page_stride16 * 16 + head_off +
                                tile * F::kTileBytes;
-            const uint8_t* k0 = p.kpages + off;
-            const uint8_t* v0 = p.vpages + off;
+            // where the unit's bytes lie: those before kTileBytes from off, the others from off1
+            size_t off1 = off;
+            if (two && left > 16)
+                off1 = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page1))) * page_stride16 * 16 + head_off - F::kTileBytes;
             const uint32_t dst = ring_lane + s_load * C::kStageBytes;
-            if (!two && left >= KT) {  // one run of bytes
+            const int bytes = left > 16 ? C::kHalf : F::kTileBytes;
 #pragma unroll
-                for (int i = 0; i < C::kHalf; i += 512) {
-                    if (i + 512 <= C::kHalf || lane * 16 < C::kHalf - i) {
-                        copy16(dst + i, k0 + i);
-                        copy16(dst + C::kHalf + i, v0 + i);
-                    }
-                }
-            } else {
-                for (int kb = 0; kb < NB && kb * 16 < left; ++kb) {
-                    if (two && kb == 1) {
-                        if (static_cast<unsigned>(page1) >= static_cast<unsigned>(p.num_pages)) {
-                            atomicCAS(p.status, 0, FA_ERR_PAGE);
-                            page1 = 0;
-                        }
-                        const size_t to = (static_cast<int64_t>(page1) - page0) * page_stride16 * 16 - F::kTileBytes;
-                        k0 += to;
-                        v0 += to;
-                    }
-                    for (int i = kb * F::kTileBytes; lane * 16 + i < (kb + 1) * F::kTileBytes; i += 512) {
-                        copy16(dst + i, k0 + i);
-                        copy16(dst + C::kHalf + i, v0 + i);
-                    }
+            for (int i = 0; i < C::kHalf; i += 512) {
+                const size_t at = i + 512 <= F::kTileBytes ? off : i >= F::kTileBytes || i + lane * 16 >= F::kTileBytes ? off1 : off;
+                if ((i + 512 <= F::kTileBytes) || i + lane * 16 < bytes) {
+                    copy16(dst + i, p.kpages + at + i);
+                    copy16(dst + C::kHalf + i, p.vpages + at + i);
                 }
             }
             ++v_load;
@@ -371,6 +361,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     if (lane < 2) parts[2 * warp + lane].kind = 0;
     __syncwarp();
     const int r = lane >> 2, t = lane & 3;
+    // V's parameters: thread (pair, group) of 32 / NG pairs at once, pair 8 kb + 2 k4 + x being keys k4 + 8 x and + 4 of tile kb
+    const int pair_group = lane % NG;
+    auto pair_of = [&](int i) { return i * (32 / NG) + lane / NG; };
+    auto pair_key = [&](int i) { return (pair_of(i) / 2) % 4 + 8 * (pair_of(i) % 2); };
     float* sc = reinterpret_cast<float*>(smem + C::kScoreOff + warp * C::kScoreBytes);  // [head][key]: scores
     uint8_t* par = smem + C::kParOff + warp * C::kParBytes;
     int s = 0;
@@ -384,14 +378,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         float o[NT][D / 16][4];
         float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u lo of group r, sums of u
         float m[NT], l[NT];
-        int E = -1000;
+        int E = -100;
+        float down = 0.0f;        // 2^-E
+        uint32_t top_limit = 0;   // the least V parameter (as fp32 bits) that 2^E does not cover
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
         uint32_t qz[NT][C::kZSteps][2];  // sums of q over a group, as the B operand of the lo product
         float A[NT][2];                  // of the score fragment's heads 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt] = -INFINITY;
+            m[nt] = kNoMax;
             l[nt] = 0.0f;
             oc[nt][0] = oc[nt][1] = oc[nt][2] = oc[nt][3] = 0.0f;
 #pragma unroll
@@ -549,35 +545,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
                 }
             }
-            // V's parameters: lane l has words NG / 2 l and on of a tile's 16 NG.  All are below 2^E.
-            uint32_t pw[NB][NG / 2], top = 0;
+            // V's parameters: a thread has those of a group of two keys, 4 apart, for each i.  All are below 2^E.
+            uint32_t pw[C::kPairs][2], top = 0;
 #pragma unroll
-            for (int kb = 0; kb < NB; ++kb) {
-                lds_words(pw[kb], vs + kb * F::kTileBytes + F::kParamOff + lane * (NG / 2 * 4));
+            for (int i = 0; i < C::kPairs; ++i) {
+                const int kb = pair_of(i) / 8, j = pair_key(i);
+                const uint8_t* from = vs + kb * F::kTileBytes + F::kParamOff + j * F::kParamBytes + pair_group * 4;
 #pragma unroll
-                for (int i = 0; i < NG / 2; ++i) top = max(top, max(pw[kb][i], (pw[kb][i] << 16) & 0x7FFF0000u));
+                for (int x = 0; x < 2; ++x) {
+                    pw[i][x] = *reinterpret_cast<const uint32_t*>(from + x * 4 * F::kParamBytes);
+                    top = max(top, max(pw[i][x], (pw[i][x] << 16) & 0x7FFF0000u));
+                }
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            if (top >= 0x7F800000u) {  // a group stands for NaN: E goes by the others
-                top = 0;
-#pragma unroll
-                for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < NG / 2; ++i) {
-                        const uint32_t hi = pw[kb][i] & 0x7FFF0000u, lo = (pw[kb][i] << 16) & 0x7FFF0000u;
-                        top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
-                    }
-                top = __reduce_max_sync(0xffffffffu, top);
-            }
-            const int e_unit = min(max(static_cast<int>(top >> 23) - 126, -100), 126);
             __syncwarp();
             // ---- softmax: thread (head r, t) takes keys t, t + 4, t + 8, t + 12 of each block
-            float u[NT][4 * NB];
-            bool grow = e_unit > E;
-            float m_new[NT];
+            float u[NT][4 * NB], mx[NT];
+            bool grow = top >= top_limit;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float mx = -INFINITY;
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) {
                     const float4 x = *reinterpret_cast<const float4*>(sc + (nt * 8 + r) * C::kScoreStride + kb * 16 + 4 * t);
@@ -588,20 +574,32 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     for (int i = 0; i < 4 * NB; ++i)
                         if ((i >> 2) * 16 + (i & 3) * 4 + t >= valid) u[nt][i] = -INFINITY;
                 }
+                mx[nt] = u[nt][0];
 #pragma unroll
-                for (int i = 0; i < 4 * NB; ++i) mx = fmaxf(mx, u[nt][i]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                m_new[nt] = fmaxf(m[nt], mx);
-                grow |= m[nt] == -INFINITY ? m_new[nt] != -INFINITY : m_new[nt] - m[nt] > kGrowBits;
+                for (int i = 1; i < 4 * NB; ++i) mx[nt] = fmaxf(mx[nt], u[nt][i]);
+                mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 1));
+                mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 2));
+                grow |= mx[nt] > m[nt] + kGrowBits;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                const int e_new = max(E, e_unit);
+                if (top >= 0x7F800000u) {  // a group stands for NaN: E goes by the others
+                    top = 0;
+#pragma unroll
+                    for (int i = 0; i < C::kPairs; ++i)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t hi = pw[i][x] & 0x7FFF0000u, lo = (pw[i][x] << 16) & 0x7FFF0000u;
+                            top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
+                        }
+                    top = __reduce_max_sync(0xffffffffu, top);
+                }
+                const int e_new = max(E, min(max(static_cast<int>(top >> 23) - 126, -100), 126));
                 const float fall = ex2_approx(static_cast<float>(E - e_new));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float alpha = m[nt] == -INFINITY ? 0.0f : ex2_approx(m[nt] - m_new[nt]);
-                    m[nt] = m_new[nt];
+                    const float m_new = fmaxf(m[nt], mx[nt]);
+                    const float alpha = ex2_approx(m[nt] - m_new);
+                    m[nt] = m_new;
                     l[nt] *= alpha;
                     const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
                     oc[nt][0] *= al0 * fall;
@@ -617,27 +615,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     }
                 }
                 E = e_new;
+                down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
+                top_limit = E == 126 ? 0x7F800000u : static_cast<uint32_t>(E + 127) << 23;
             }
-            {
-                // lane l: key l / 2's parameters of groups NG / 2 (l % 2) and on, into the order the products want
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
-                const int k4 = (lane / 2) % 4, ki = lane / 8, g0 = (lane % 2) * (NG / 2);
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb) {
-                    uint8_t* s_to = par + ((kb * 4 + k4) * NG + g0) * 8 + ki * 2;
-                    uint8_t* z_to = par + C::kSBytes + (kb * NG + g0) * 32 + k4 * 8 + ki * 2;
-#pragma unroll
-                    for (int i = 0; i < NG / 2; ++i) {
-                        const uint32_t sz = pack_f16x2(s_of(pw[kb][i]) * down, lo_of(pw[kb][i]) * down);
-                        *reinterpret_cast<uint16_t*>(s_to + i * 8) = static_cast<uint16_t>(sz);
-                        *reinterpret_cast<uint16_t*>(z_to + i * 32) = static_cast<uint16_t>(sz >> 16);
-                    }
-                }
+            for (int i = 0; i < C::kPairs; ++i) {
+                const int kb = pair_of(i) / 8, j = pair_key(i);
+                uint8_t* s_to = par + ((kb * 4 + j % 4) * NG + pair_group) * 8 + j / 8 * 4;
+                uint8_t* z_to = par + C::kSBytes + (kb * NG + pair_group) * 32 + (j % 4) * 8 + j / 8 * 4;
+                *reinterpret_cast<uint32_t*>(s_to) = pack_f16x2(s_of(pw[i][0]) * down, s_of(pw[i][1]) * down);
+                *reinterpret_cast<uint32_t*>(z_to) = pack_f16x2(lo_of(pw[i][0]) * down, lo_of(pw[i][1]) * down);
             }
             uint32_t uh[NT][NB][2];  // the weights in fp16: keys (t, t + 4) and (t + 8, t + 12)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float bias = kRefBits - (m[nt] == -INFINITY ? 0.0f : m[nt]);
+                const float bias = kRefBits - m[nt];
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) {
                     float* x = u[nt] + 4 * kb;
@@ -721,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
             l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
             // no finite score (only NaN and -inf): l says so
-            const float lse = (m[nt] == -INFINITY ? 0.0f : m[nt]) - kRefBits + log2f(l[nt]);
+            const float lse = m[nt] - kRefBits + log2f(l[nt]);
             const int h = nt * 8 + r;
             if (t == 0 && h < G) {
                 if (whole) p.lse[head0 + h] = lse * 0.6931471805599453f;
