@@ -15,9 +15,9 @@
 // head so that its largest value is in [2^14, 2^15): fp16 then holds every bf16 of
 // it exactly down to 2^-29 of that, and to 2^-40 in absolute terms.
 //
-// Weights.  u = 2^7 2^(x - m), below 2^15 because the reference m follows the maximum to
+// Weights.  u = 2^6 2^(x - m), below 2^14 because the reference m follows the maximum to
 // within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head.  lo
-// and s are scaled by 2^-E, which makes the greatest of a unit less than 1, so fp16 holds
+// and s are scaled by 2^-E, which keeps those of every unit below 2, so fp16 holds
 // their 8 bits down to 2^-17 of that; u s is rounded to fp16 again, u lo is not.  One
 // product of the rounded u with [lo of each group; ones] gives the sums of u lo and of u: the output is
 // divided by the sum of the same rounded weights, so their errors only weigh values
@@ -60,7 +60,7 @@ constexpr int kThreads = 32 * NC;
 // CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone takes nt d / 4.
 __host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
-constexpr float kRefBits = 7.0f;    // u is 2^kRefBits at the running maximum
+constexpr float kRefBits = 6.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 constexpr float kNoMax = -1e30f;    // the maximum of no score: finite, so that no difference is NaN
 
@@ -379,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u lo of group r, sums of u
         float m[NT], l[NT];
         int E = -100;
-        float down = 0.0f;        // 2^-E
-        uint32_t top_limit = 0;   // the least V parameter (as fp32 bits) that 2^E does not cover
+        float down = 0.0f;  // 2^-E
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
         uint32_t qz[NT][C::kZSteps][2];  // sums of q over a group, as the B operand of the lo product
@@ -545,23 +544,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
                 }
             }
-            // V's parameters: a thread has those of a group of two keys, 4 apart, for each i.  All are below 2^E.
-            uint32_t pw[C::kPairs][2], top = 0;
+            // V's parameters over 2^E: a thread converts those of a group of two keys, 4 apart, for each i.
+            // fp16 bit 14 tells a value of 2 or more, an infinity or NaN: then E has to be looked at below.
+            uint32_t over = 0;
+            auto convert = [&]() {
 #pragma unroll
-            for (int i = 0; i < C::kPairs; ++i) {
-                const int kb = pair_of(i) / 8, j = pair_key(i);
-                const uint8_t* from = vs + kb * F::kTileBytes + F::kParamOff + j * F::kParamBytes + pair_group * 4;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    pw[i][x] = *reinterpret_cast<const uint32_t*>(from + x * 4 * F::kParamBytes);
-                    top = max(top, max(pw[i][x], (pw[i][x] << 16) & 0x7FFF0000u));
+                for (int i = 0; i < C::kPairs; ++i) {
+                    const int kb = pair_of(i) / 8, j = pair_key(i);
+                    const uint8_t* from = vs + kb * F::kTileBytes + F::kParamOff + j * F::kParamBytes + pair_group * 4;
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(from);
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(from + 4 * F::kParamBytes);
+                    const uint32_t sp = pack_f16x2(s_of(x) * down, s_of(y) * down), zp = pack_f16x2(lo_of(x) * down, lo_of(y) * down);
+                    over |= sp | zp;
+                    *reinterpret_cast<uint32_t*>(par + ((kb * 4 + j % 4) * NG + pair_group) * 8 + j / 8 * 4) = sp;
+                    *reinterpret_cast<uint32_t*>(par + C::kSBytes + (kb * NG + pair_group) * 32 + (j % 4) * 8 + j / 8 * 4) = zp;
                 }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
+            };
+            convert();
             __syncwarp();
             // ---- softmax: thread (head r, t) takes keys t, t + 4, t + 8, t + 12 of each block
             float u[NT][4 * NB], mx[NT];
-            bool grow = top >= top_limit;
+            bool grow = (over & 0x40004000u) != 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -582,17 +585,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 grow |= mx[nt] > m[nt] + kGrowBits;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                if (top >= 0x7F800000u) {  // a group stands for NaN: E goes by the others
-                    top = 0;
+                uint32_t top = 0;  // greatest magnitude of the unit's parameters, as fp32 bits; NaN left out
 #pragma unroll
-                    for (int i = 0; i < C::kPairs; ++i)
+                for (int i = 0; i < C::kPairs; ++i)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t hi = pw[i][x] & 0x7FFF0000u, lo = (pw[i][x] << 16) & 0x7FFF0000u;
-                            top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
-                        }
-                    top = __reduce_max_sync(0xffffffffu, top);
-                }
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                            vs + (pair_of(i) / 8) * F::kTileBytes + F::kParamOff + (pair_key(i) + 4 * x) * F::kParamBytes + pair_group * 4);
+                        const uint32_t hi = w & 0x7FFF0000u, lo = (w << 16) & 0x7FFF0000u;
+                        top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
+                    }
+                top = __reduce_max_sync(0xffffffffu, top);
                 const int e_new = max(E, min(max(static_cast<int>(top >> 23) - 126, -100), 126));
                 const float fall = ex2_approx(static_cast<float>(E - e_new));
 #pragma unroll
@@ -616,15 +619,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 }
                 E = e_new;
                 down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
-                top_limit = E == 126 ? 0x7F800000u : static_cast<uint32_t>(E + 127) << 23;
-            }
-#pragma unroll
-            for (int i = 0; i < C::kPairs; ++i) {
-                const int kb = pair_of(i) / 8, j = pair_key(i);
-                uint8_t* s_to = par + ((kb * 4 + j % 4) * NG + pair_group) * 8 + j / 8 * 4;
-                uint8_t* z_to = par + C::kSBytes + (kb * NG + pair_group) * 32 + (j % 4) * 8 + j / 8 * 4;
-                *reinterpret_cast<uint32_t*>(s_to) = pack_f16x2(s_of(pw[i][0]) * down, s_of(pw[i][1]) * down);
-                *reinterpret_cast<uint32_t*>(z_to) = pack_f16x2(lo_of(pw[i][0]) * down, lo_of(pw[i][1]) * down);
+                __syncwarp();  // the scores have been read: not before the parameters are written anew
+                convert();
             }
             uint32_t uh[NT][NB][2];  // the weights in fp16: keys (t, t + 4) and (t + 8, t + 12)
 #pragma unroll
@@ -680,10 +676,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                             uint32_t a0, a1, a2, a3;
                             if constexpr (BITS == 4) {
                                 const int sel = gp % 2 ? 0x7632 : 0x5410;
-                                const uint32_t x = __byte_perm(c[0][w], c[1][w], sel) >> (8 * st);
-                                const uint32_t y = __byte_perm(c[2][w], c[3][w], sel) >> (8 * st);
-                                a0 = x & 0x000F000Fu, a1 = x & 0x00F000F0u;
-                                a2 = y & 0x000F000Fu, a3 = y & 0x00F000F0u;
+                                // the low row is given both nibbles of its bytes, 16 hi + lo; the high row's sum
+                                // is taken off it at the end
+                                const uint32_t x = __byte_perm(c[0][w], c[1][w], sel);
+                                const uint32_t y = __byte_perm(c[2][w], c[3][w], sel);
+                                a0 = st ? __byte_perm(x, 0, 0x4341) : x & 0x00FF00FFu, a1 = a0 & 0x00F000F0u;
+                                a2 = st ? __byte_perm(y, 0, 0x4341) : y & 0x00FF00FFu, a3 = a2 & 0x00F000F0u;
                             } else {
                                 const int sel = st ? 0x7632 : 0x5410;
                                 const uint32_t x = __byte_perm(c[0][w], c[1][w], sel);
@@ -729,8 +727,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const float z = __shfl_sync(0xffffffffu, oc[nt][c], 4 * g + t);
-                    const float* o0 = o[nt][2 * g];
-                    const float* o1 = o[nt][2 * g + 1];
+                    float* o0 = o[nt][2 * g];
+                    float* o1 = o[nt][2 * g + 1];
+                    if (BITS == 4) o0[c] -= o0[c + 2], o1[c] -= o1[c + 2];
                     float4 x = make_float4(fmaf(o0[c], kUp, z) * inv * scale_e, fmaf(o0[c + 2], kUp1, z) * inv * scale_e,
                                            fmaf(o1[c], kUp, z) * inv * scale_e, fmaf(o1[c + 2], kUp1, z) * inv * scale_e);
                     const int d = g * kKvqGroup + 4 * r;
