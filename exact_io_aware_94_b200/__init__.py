@@ -17,6 +17,7 @@ Two levels:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -392,39 +393,56 @@ def forward_blocksparse(q, k, v, block_mask, scale=None, causal=False, out_dtype
 KVQ_GROUP = 32
 
 
-def _kvq_page_size(kpages, vpages, d, bits):
-    """Page size of a pair of pools, from the bytes of a page and KV head."""
-    for t, n in ((kpages, "kpages"), (vpages, "vpages")):
-        _need(t, n, torch.uint8)
+_kvq_sizes = functools.lru_cache(maxsize=1024)(fa_decode_paged_quant_workspace_size)
+
+
+def _kvq_check(dev, *named):
+    """Raises unless each (tensor, name, dtype) is a contiguous tensor of that type on CUDA device `dev`."""
+    for t, name, dtype in named:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s" % (name, dtype))
+        if t.get_device() != dev:
+            raise ValueError("%s must be on device %d, as the other tensors are" % (name, dev))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _kvq_device(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits):
+    """(page size, sequences, table width) of a pair of pools and their table, checked."""
+    _kvq_check(dev, (kpages, "kpages", torch.uint8), (vpages, "vpages", torch.uint8),
+               (block_table, "block_table", torch.int32), (kv_lens, "kv_lens", torch.int32))
     if kpages.dim() != 3 or kpages.shape != vpages.shape:
         raise ValueError("kpages and vpages must both be [num_pages, Hkv, page_bytes]")
+    if block_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
     if d not in (64, 128, 256) or bits not in (4, 8):
         raise FAError(FA_ERR_UNSUPPORTED, "quantised cache with d = %r, bits = %r" % (d, bits))
     page_size, rest = divmod(kpages.shape[2], d * bits // 8 + d // KVQ_GROUP * 4)
     if rest or page_size == 0:
         raise ValueError("a page of %d bytes is not whole tokens of d = %d in %d bits" % (kpages.shape[2], d, bits))
-    return page_size
+    return (page_size,) + tuple(block_table.shape)
 
 
-def _kvq_call(first, stream, tensors):
-    """Checks that every tensor is on the first one's device.  The calls below run with that device current and, if a
-    stream is given, with it current too, so that what they allocate belongs to the stream that uses it."""
-    for t in tensors:
-        if t.device != first.device:
-            raise ValueError("all tensors must be on %s" % first.device)
+def _kvq_run(dev, stream, call):
+    """call(stream handle) with `dev` current and, if a stream is given, that stream too: what the call allocates
+    then belongs to the stream that uses it."""
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(int(stream), device=first.device)
-        return torch.cuda.stream(s)
-    return torch.cuda.device(first.device)
-
-
-def _kvq_table(block_table, kv_lens):
-    _need(block_table, "block_table", torch.int32)
-    _need(kv_lens, "kv_lens", torch.int32)
-    if block_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != block_table.shape[0]:
-        raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
-    return block_table.shape
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return call(torch._C._cuda_getCurrentRawStream(dev))
+    return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def kvcache_quant_pages(num_pages, Hkv, page_size, d, bits, device="cuda"):
@@ -439,71 +457,81 @@ def kvcache_append_quant(k, v, kpages, vpages, cu_seqlens_new, block_table, kv_l
     """Quantises k, v [total_new, Hkv, d] (bf16; rows may be strided, as slices of a fused projection are) into the last
     positions of each sequence: rows [cu_seqlens_new[b], cu_seqlens_new[b+1]) become positions up to kv_lens[b] (the
     length after the append).  cu_seqlens_new int32 [B+1], block_table int32 [B,max_blocks], kv_lens int32 [B]."""
+    dev = _kvq_device(k, "k")
     strides = []
     for t, n in ((k, "k"), (v, "v")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
-            raise ValueError("%s must be a CUDA bfloat16 tensor [total_new, Hkv, d]" % n)
+        if _kvq_device(t, n) != dev or t.dtype != torch.bfloat16 or t.dim() != 3:
+            raise ValueError("%s must be a bfloat16 tensor [total_new, Hkv, d] on device %d" % (n, dev))
         T, Hkv, d = t.shape
-        if (d > 1 and t.stride(2) != 1) or (Hkv > 1 and t.stride(1) != d):
+        s = t.stride()
+        if (d > 1 and s[2] != 1) or (Hkv > 1 and s[1] != d):
             raise ValueError("the heads of a row of %s must be contiguous" % n)
-        strides.append(t.stride(0) if T > 1 else Hkv * d)
+        strides.append(s[0] if T > 1 else Hkv * d)
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
-    page_size = _kvq_page_size(kpages, vpages, d, bits)
-    _need(cu_seqlens_new, "cu_seqlens_new", torch.int32)
-    B, max_blocks = _kvq_table(block_table, kv_lens)
-    if cu_seqlens_new.numel() != B + 1 or kpages.shape[1] != Hkv:
+    page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
+    _kvq_check(dev, (cu_seqlens_new, "cu_seqlens_new", torch.int32))
+    if cu_seqlens_new.shape != (B + 1,) or kpages.shape[1] != Hkv:
         raise ValueError("cu_seqlens_new must be [B + 1] and the pools' KV heads k's")
     if T == 0:
         return
-    with _kvq_call(k, stream, (v, kpages, vpages, cu_seqlens_new, block_table, kv_lens)):
-        rc = fa_kvcache_append_quant(k, v, strides[0], strides[1], kpages, vpages, cu_seqlens_new, block_table, kv_lens, B,
-                                     Hkv, T, int(max_seqlen_new), kpages.shape[0], page_size, max_blocks, d, bits, stream)
-    _check(rc, "fa_kvcache_append_quant")
+    _check(_kvq_run(dev, stream, lambda handle: load_library().fa_kvcache_append_quant(
+        k.data_ptr(), v.data_ptr(), strides[0], strides[1], kpages.data_ptr(), vpages.data_ptr(),
+        cu_seqlens_new.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), B, Hkv, T, int(max_seqlen_new),
+        kpages.shape[0], page_size, max_blocks, d, bits, handle)), "fa_kvcache_append_quant")
 
 
 def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, max_seqlen, H, d, bits,
                        out_dtype=torch.bfloat16, stream=None):
     """The last cu_seqlens[b+1] - cu_seqlens[b] rows of each sequence as k, v [total, H, d] (out_dtype), KV head
     h / (H / Hkv) for head h: what forward_varlen takes."""
-    page_size = _kvq_page_size(kpages, vpages, d, bits)
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    B, max_blocks = _kvq_table(block_table, kv_lens)
-    if cu_seqlens.numel() != B + 1:
+    dev = _kvq_device(kpages, "kpages")
+    page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
+    _kvq_check(dev, (cu_seqlens, "cu_seqlens", torch.int32))
+    if cu_seqlens.shape != (B + 1,):
         raise ValueError("cu_seqlens must be [B + 1]")
-    num_pages, Hkv = kpages.shape[:2]
-    with _kvq_call(kpages, stream, (vpages, cu_seqlens, block_table, kv_lens)):
+    total = int(total)
+
+    def call(handle):
         k = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
-        v = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
-        if total == 0:
-            return k, v
-        rc = fa_kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, k, v, B, H, Hkv, int(total),
-                                   int(max_seqlen), num_pages, page_size, max_blocks, d, bits, _DT[out_dtype], stream)
-    _check(rc, "fa_kvcache_read_quant")
-    return k, v
+        v = torch.empty_like(k)
+        if total:
+            _check(load_library().fa_kvcache_read_quant(
+                kpages.data_ptr(), vpages.data_ptr(), cu_seqlens.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+                k.data_ptr(), v.data_ptr(), B, H, kpages.shape[1], total, int(max_seqlen), kpages.shape[0], page_size,
+                max_blocks, d, bits, _DT[out_dtype], handle), "fa_kvcache_read_quant")
+        return k, v
+
+    return _kvq_run(dev, stream, call)
 
 
 def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None, out_dtype=torch.float32, ws=None,
                        stream=None):
     """decode_paged over a quantised cache: o [B,H,d] and lse [B,H] for q [B,H,d] (bf16), pools
     [num_pages,Hkv,page bytes] (uint8), block_table int32 [B,max_blocks] and kv_lens int32 [B] (device)."""
-    _need(q, "q")
+    dev = _kvq_device(q, "q")
+    _kvq_check(dev, (q, "q", torch.bfloat16))
     if q.dim() != 3:
         raise ValueError("q must be [B, H, d]")
     B, H, d = q.shape
-    page_size = _kvq_page_size(kpages, vpages, d, bits)
-    if _kvq_table(block_table, kv_lens)[0] != B:
+    page_size, rows, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
+    if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
-    num_pages, Hkv = kpages.shape[:2]
-    max_blocks = block_table.shape[1]
-    with _kvq_call(q, stream, (kpages, vpages, block_table, kv_lens) + (() if ws is None else (ws,))):
-        nbytes = fa_decode_paged_quant_workspace_size(B, H, Hkv, max_blocks, page_size, d, bits)
-        if ws is None:
-            ws = workspace(nbytes, q.device)
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != dev):
+        raise ValueError("ws must be a tensor on device %d" % dev)
+    Hkv = kpages.shape[1]
+
+    def call(handle):
+        w = ws
+        if w is None:
+            w = workspace(_kvq_sizes(B, H, Hkv, max_blocks, page_size, d, bits), q.device)
         o = torch.empty((B, H, d), dtype=out_dtype, device=q.device)
         lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        rc = fa_decode_paged_quant(q, kpages, vpages, block_table, kv_lens, o, lse, B, H, Hkv, num_pages, page_size,
-                                   max_blocks, d, bits, 1.0 / math.sqrt(d) if scale is None else scale, _DT[out_dtype],
-                                   ws, ws.numel() * ws.element_size(), stream)
-    _check(rc, "fa_decode_paged_quant")
-    return o, lse
+        _check(load_library().fa_decode_paged_quant(
+            q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
+            lse.data_ptr(), B, H, Hkv, kpages.shape[0], page_size, max_blocks, d, bits,
+            1.0 / math.sqrt(d) if scale is None else scale, _DT[out_dtype], w.data_ptr(), w.numel() * w.element_size(),
+            handle), "fa_decode_paged_quant")
+        return o, lse
+
+    return _kvq_run(dev, stream, call)

@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -914,10 +915,17 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
 }
 
 template <int D, int BITS, int NT>
-cudaError_t launch(const DecodeQuantParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_t stream) {
     using C = Cfg<D, BITS, NT>;
-    cudaError_t e = cudaFuncSetAttribute(fa_decode_quant_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
+    static std::atomic<uint64_t> ready{0};  // a bit a device whose kernel has its shared memory set
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) & bit)) {
+        if ((e = cudaFuncSetAttribute(fa_decode_quant_split<D, BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      C::kBytes)) != cudaSuccess)
+            return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
     const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
     fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
@@ -1009,10 +1017,10 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.o_dtype = o_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (d == 256) e = bits == 4 ? launch<256, 4, 1>(p, num_sms, s) : launch<256, 8, 1>(p, num_sms, s);
-    else if (d == 128 && nt == 1) e = bits == 4 ? launch<128, 4, 1>(p, num_sms, s) : launch<128, 8, 1>(p, num_sms, s);
-    else if (d == 128) e = bits == 4 ? launch<128, 4, 2>(p, num_sms, s) : launch<128, 8, 2>(p, num_sms, s);
-    else if (nt == 1) e = bits == 4 ? launch<64, 4, 1>(p, num_sms, s) : launch<64, 8, 1>(p, num_sms, s);
-    else e = bits == 4 ? launch<64, 4, 2>(p, num_sms, s) : launch<64, 8, 2>(p, num_sms, s);
+    if (d == 256) e = bits == 4 ? launch<256, 4, 1>(p, dev, num_sms, s) : launch<256, 8, 1>(p, dev, num_sms, s);
+    else if (d == 128 && nt == 1) e = bits == 4 ? launch<128, 4, 1>(p, dev, num_sms, s) : launch<128, 8, 1>(p, dev, num_sms, s);
+    else if (d == 128) e = bits == 4 ? launch<128, 4, 2>(p, dev, num_sms, s) : launch<128, 8, 2>(p, dev, num_sms, s);
+    else if (nt == 1) e = bits == 4 ? launch<64, 4, 1>(p, dev, num_sms, s) : launch<64, 8, 1>(p, dev, num_sms, s);
+    else e = bits == 4 ? launch<64, 4, 2>(p, dev, num_sms, s) : launch<64, 8, 2>(p, dev, num_sms, s);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
