@@ -2,8 +2,9 @@
 // fa_kvcache_read_quant (declared in include/fa.h, format in kvquant.cuh).
 //
 // Both are one pass over the rows that they touch.  A block takes 16 tokens of one
-// sequence, all KV heads, K and V; a thread takes 8 consecutive dimensions of a
-// token's head (16 bytes of bf16), and the four threads of a 32-value group find
+// sequence, all KV heads, K and V.  A warp takes 256 consecutive values of a token's
+// row at a time, K and V: a thread has 8 consecutive dimensions (16 bytes of bf16)
+// and always the same ones of a head, and the four threads of a 32-value group find
 // its least and largest value with two shuffles.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,40 +72,50 @@ __device__ __forceinline__ void kvq_pages(const KvqParams& p, int b, int n, int 
     __syncthreads();
 }
 
-// Byte offset in a tile of unit `u` of the group that holds 8-dimension chunk c, for token row r.
+// Byte offset in a tile of unit `u` of the group that holds 8-dimension chunk c, for token row 0.
 template <int D, int BITS, int U>
-__device__ __forceinline__ int kvq_code_off(int r, int c, int u) {
+__device__ __forceinline__ int kvq_code_off(int c, int u) {
     using F = KvqFormat<D, BITS>;
     const int plane = c / (F::kPlaneDims / 8), g = (c % (F::kPlaneDims / 8)) >> 2;
-    return plane * (kKvqTile * F::kPlaneBytes) + r * F::kPlaneBytes + (u * F::kPlaneGroups + g) * (U * BITS / 8);
+    return plane * (kKvqTile * F::kPlaneBytes) + (u * F::kPlaneGroups + g) * (U * BITS / 8);
 }
+
+// The block's items: (token, 256 values of its row), dealt to the warps in turn.
+struct KvqItems {
+    int token, part, parts;
+    __device__ __forceinline__ KvqItems(int warp, int parts_) : token(0), part(warp), parts(parts_) { wrap(); }
+    __device__ __forceinline__ void wrap() {
+        while (part >= parts) part -= parts, ++token;
+    }
+    __device__ __forceinline__ void next() {
+        part += kKvqThreads / 32;
+        wrap();
+    }
+};
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
 // Quantises the thread's 8 values.  Every thread of the warp takes part in the shuffles.
 // Each step of the format's definition is one fp32 operation rounded to nearest, so
-// none may be contracted into another.
+// none may be contracted into another.  An infinity or NaN anywhere in the group makes
+// hi - lo, and with it s, infinite or NaN (the minimum and maximum pass NaN on).
 template <int BITS>
 __device__ __forceinline__ void kvq_quantise(const uint4& raw, uint32_t (&code)[2], uint32_t& param) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-    float lo = x[0], hi = x[0];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad |= !(fabsf(x[i]) <= FLT_MAX);
-    }
-    if (bad) hi = INFINITY, lo = -INFINITY;
+    __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
+    __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
+    // lo in the low half, hi in the high half, each over the thread's 8 values
+    lo2 = __hmin2_nan(lo2, __lowhigh2highlow(lo2));
+    hi2 = __hmax2_nan(hi2, __lowhigh2highlow(hi2));
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(as_word(lo2), as_word(hi2), 0x7610), o);
+        lo2 = __hmin2_nan(lo2, as_bf162(other));  // low half
+        hi2 = __hmax2_nan(hi2, as_bf162(other));  // high half
     }
+    float lo = __uint_as_float(as_word(lo2) << 16);
+    const float hi = __uint_as_float(as_word(hi2) & 0xFFFF0000u);
     constexpr float kMax = static_cast<float>((1 << BITS) - 1);
     float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), kMax)));
     if (!(s <= FLT_MAX)) {
@@ -113,21 +124,30 @@ __device__ __forceinline__ void kvq_quantise(const uint4& raw, uint32_t (&code)[
     } else if (s < FLT_MIN) {
         s = 0.0f;  // 1 / s would overflow
     }
-    const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+    const uint32_t keep = s > 0.0f ? 0xFFFFFFFFu : 0u;
     uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        const float x = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        float t = __fmul_rn(__fsub_rn(x, lo), inv);
+        // s is at least (1 - 2^-8) of the exact step: 15 / (1 - 2^-8) still rounds to 15, 255 / (1 - 2^-8) to 256
+        if (BITS == 8) t = fminf(t, kMax);
         // 2^23 + 2^22 has an ulp of 1: the sum's low bits are the nearest integer
-        float t = fminf(__fmul_rn(__fsub_rn(x[i], lo), inv), kMax);
-        t = s > 0.0f ? t : 0.0f;
-        c[i] = __float_as_uint(__fadd_rn(t, 12582912.0f)) & 0xFFu;
+        c[i] = __float_as_uint(__fadd_rn(t, 12582912.0f));
     }
+    constexpr uint32_t kMagic = 0x4B400000u;  // the bits of 2^23 + 2^22
     if constexpr (BITS == 4) {
-        code[0] = c[0] | (c[1] << 4) | (c[2] << 8) | (c[3] << 12) | (c[4] << 16) | (c[5] << 20) | (c[6] << 24) | (c[7] << 28);
+        uint32_t x = c[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) x += c[i] << (4 * i);
+        code[0] = (x - kMagic * 0x11111111u) & keep;
         code[1] = 0;
     } else {
-        code[0] = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-        code[1] = c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            code[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+                                  0x5410) & keep;
     }
     param = (__float_as_uint(lo) >> 16) | (__float_as_uint(s) & 0xFFFF0000u);
 }
@@ -140,22 +160,35 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) 
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
     kvq_pages(p, b, n, pos0, s_page);
-    constexpr int C = D / 8;  // threads of a row
-    const int total = n * p.Hkv * C;
+    constexpr int C = D / 8;       // threads of a head
+    constexpr int HW = 32 / C;     // heads of an item
+    const int lane = threadIdx.x & 31;
+    const int c = lane % C, u = c & 3, h0 = lane / C;
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    // whole warps stay in the loop for the shuffles; 8 divides the tasks of a token, so groups of 4 never split
-    for (int t0 = 0; t0 < total; t0 += kKvqThreads) {
-        const int t = t0 + threadIdx.x;
-        const bool live = t < total;
-        const int tt = live ? t : 0;
-        const int c = tt % C, row = tt / C;
-        const int i = row / p.Hkv, h = row - i * p.Hkv;
-        const int at = h * D + c * 8;
-        const uint4 kr = *reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + at);
-        const uint4 vr = *reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + at);
+    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(c, u);
+    // V's units 2 u and 2 u + 1 of this group: of two neighbouring groups the even one writes unit 2 u of both,
+    // the odd one unit 2 u + 1
+    const bool odd = (c >> 2) & 1;
+    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>(c & ~4, 2 * u + odd);
+    const int p_off = F::kParamOff + (c >> 2) * 4;
+    for (KvqItems it(threadIdx.x >> 5, (p.Hkv + HW - 1) / HW); it.token < n; it.next()) {
+        const int i = it.token, h = it.part * HW + h0;
+        const bool live = h < p.Hkv;
+        const int at = (live ? h : 0) * D + c * 8;
+        const uint4 kr = __ldcs(reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + at));
+        const uint4 vr = __ldcs(reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + at));
         uint32_t kc[2], vc[2], kp, vp;
         kvq_quantise<BITS>(kr, kc, kp);
         kvq_quantise<BITS>(vr, vc, vp);
+        uint32_t vw[2];  // V's word or words to write
+        if constexpr (BITS == 4) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, vc[0], 4);
+            vw[0] = odd ? __byte_perm(other, vc[0], 0x7632) : __byte_perm(vc[0], other, 0x5410);
+        } else {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vc[0] : vc[1], 4);
+            vw[0] = odd ? other : vc[0];
+            vw[1] = odd ? vc[1] : other;
+        }
         const int pg = s_page[i];
         if (!live || pg < 0) continue;
         const int slot = (pos0 + i) & ((1 << p.page_shift) - 1), r = slot % kKvqTile;
@@ -163,53 +196,61 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) 
                            static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
         uint8_t* kt = p.kpages + off;
         uint8_t* vt = p.vpages + off;
-        const int u = c & 3;
-        uint8_t* kd = kt + kvq_code_off<D, BITS, kKvqUnitK>(r, c, u);
-        uint8_t* v0 = vt + kvq_code_off<D, BITS, kKvqUnitV>(r, c, 2 * u);
-        uint8_t* v1 = vt + kvq_code_off<D, BITS, kKvqUnitV>(r, c, 2 * u + 1);
+        uint8_t* kd = kt + k_off + r * F::kPlaneBytes;
+        uint8_t* vd = vt + v_off + r * F::kPlaneBytes;
         if constexpr (BITS == 4) {
             *reinterpret_cast<uint32_t*>(kd) = kc[0];
-            *reinterpret_cast<uint16_t*>(v0) = static_cast<uint16_t>(vc[0]);
-            *reinterpret_cast<uint16_t*>(v1) = static_cast<uint16_t>(vc[0] >> 16);
+            *reinterpret_cast<uint32_t*>(vd) = vw[0];
         } else {
             *reinterpret_cast<uint2*>(kd) = make_uint2(kc[0], kc[1]);
-            *reinterpret_cast<uint32_t*>(v0) = vc[0];
-            *reinterpret_cast<uint32_t*>(v1) = vc[1];
+            *reinterpret_cast<uint2*>(vd) = make_uint2(vw[0], vw[1]);
         }
         if (u == 0) {
-            const int po = F::kParamOff + r * F::kParamBytes + (c >> 2) * 4;
-            *reinterpret_cast<uint32_t*>(kt + po) = kp;
-            *reinterpret_cast<uint32_t*>(vt + po) = vp;
+            *reinterpret_cast<uint32_t*>(kt + p_off + r * F::kParamBytes) = kp;
+            *reinterpret_cast<uint32_t*>(vt + p_off + r * F::kParamBytes) = vp;
         }
     }
 }
 
-// The 8 values lo + s c of a chunk, rounded once to fp32 and then to the output type,
-// written to the G query heads that share the KV head.
+// The 8 values lo + s c of a chunk, each rounded once to the output type, written to the
+// G query heads that share the KV head.
 template <int D, int BITS>
 __device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t param, void* out, size_t at, int G, bool f32) {
-    const float lo = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t c = BITS == 4 ? (code[0] >> (4 * i)) & 15u : (code[i >> 2] >> (8 * (i & 3))) & 255u;
-        x[i] = fmaf(s, static_cast<float>(c), lo);
-    }
     if (f32) {
+        const float lo = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t c = BITS == 4 ? (code[0] >> (4 * i)) & 15u : (code[i >> 2] >> (8 * (i & 3))) & 255u;
+            x[i] = fmaf(s, static_cast<float>(c), lo);
+        }
         float* o = static_cast<float*>(out) + at;
         for (int g = 0; g < G; ++g, o += D) {
             *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4*>(o + 4) = make_float4(x[4], x[5], x[6], x[7]);
         }
     } else {
-        uint32_t w[4];
+        const __nv_bfloat162 lo = as_bf162(__byte_perm(param, 0, 0x1010)), s = as_bf162(__byte_perm(param, 0, 0x3232));
+        uint32_t y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 two = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&two);
+            __nv_bfloat162 c;  // codes 2 i and 2 i + 1
+            if constexpr (BITS == 4) {
+                // 0x4300 | c is 128 + c in bf16
+                const uint32_t up = i < 2 ? code[0] << (12 - 8 * i) : code[0] >> (8 * i - 12);
+                const uint32_t two = ((code[0] >> (8 * i)) & 0xFu) | (up & 0xF0000u) | 0x43004300u;
+                c = __hsub2(as_bf162(two), as_bf162(0x43004300u));
+            } else {
+                // 2^23 + c in fp32; less 2^23, c fits the high half
+                const uint32_t w = code[i >> 1] >> (16 * (i & 1));
+                const float x0 = __uint_as_float(0x4B000000u | (w & 255u)) - 8388608.0f;
+                const float x1 = __uint_as_float(0x4B000000u | ((w >> 8) & 255u)) - 8388608.0f;
+                c = as_bf162(__byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632));
+            }
+            y[i] = as_word(__hfma2(s, c, lo));
         }
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at;
-        for (int g = 0; g < G; ++g, o += D) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int g = 0; g < G; ++g, o += D) *reinterpret_cast<uint4*>(o) = make_uint4(y[0], y[1], y[2], y[3]);
     }
 }
 
@@ -221,24 +262,26 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p, in
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
     kvq_pages(p, b, n, pos0, s_page);
-    constexpr int C = D / 8;
-    const int total = n * p.Hkv * C;
+    constexpr int C = D / 8, HW = 32 / C;
+    const int lane = threadIdx.x & 31;
+    const int c = lane % C, u = c & 3, h0 = lane / C;
     const int G = p.H / p.Hkv;
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    for (int t = threadIdx.x; t < total; t += kKvqThreads) {
-        const int c = t % C, row = t / C;
-        const int i = row / p.Hkv, h = row - i * p.Hkv;
+    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(c, u);
+    const int v_off0 = kvq_code_off<D, BITS, kKvqUnitV>(c, 2 * u), v_off1 = kvq_code_off<D, BITS, kKvqUnitV>(c, 2 * u + 1);
+    const int p_off = F::kParamOff + (c >> 2) * 4;
+    for (KvqItems it(threadIdx.x >> 5, (p.Hkv + HW - 1) / HW); it.token < n; it.next()) {
+        const int i = it.token, h = it.part * HW + h0;
+        if (h >= p.Hkv) continue;
         const int pg = max(s_page[i], 0);  // a bad entry is flagged and read as page 0
         const int slot = (pos0 + i) & ((1 << p.page_shift) - 1), r = slot % kKvqTile;
         const size_t off = (static_cast<size_t>(pg) * p.Hkv + h) * block_bytes +
                            static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
         const uint8_t* kt = p.kpages + off;
         const uint8_t* vt = p.vpages + off;
-        const int u = c & 3;
-        const uint8_t* kd = kt + kvq_code_off<D, BITS, kKvqUnitK>(r, c, u);
-        const uint8_t* v0 = vt + kvq_code_off<D, BITS, kKvqUnitV>(r, c, 2 * u);
-        const uint8_t* v1 = vt + kvq_code_off<D, BITS, kKvqUnitV>(r, c, 2 * u + 1);
-        const int po = F::kParamOff + r * F::kParamBytes + (c >> 2) * 4;
+        const uint8_t* kd = kt + k_off + r * F::kPlaneBytes;
+        const uint8_t* v0 = vt + v_off0 + r * F::kPlaneBytes;
+        const uint8_t* v1 = vt + v_off1 + r * F::kPlaneBytes;
         uint32_t kc[2] = {0, 0}, vc[2] = {0, 0};
         if constexpr (BITS == 4) {
             kc[0] = *reinterpret_cast<const uint32_t*>(kd);
@@ -250,8 +293,8 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p, in
             vc[0] = *reinterpret_cast<const uint32_t*>(v0);
             vc[1] = *reinterpret_cast<const uint32_t*>(v1);
         }
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + po);
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + po);
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + p_off + r * F::kParamBytes);
+        const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + p_off + r * F::kParamBytes);
         const size_t at = (static_cast<size_t>(first + i) * p.H + h * G) * D + c * 8;
         kvq_emit<D, BITS>(kc, kp, p.k_out, at, G, f32 != 0);
         kvq_emit<D, BITS>(vc, vp, p.v_out, at, G, f32 != 0);

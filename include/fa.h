@@ -287,8 +287,8 @@ int fa_kvcache_append_quant(const void* k, const void* v, long long stride_k, lo
  * cu_seqlens[b+1] - cu_seqlens[b] <= max_seqlen (n_b = kv_lens[b] reads all of
  * it).  Head h of the output is KV head h / (H / Hkv): with H query heads the
  * result is what fa_forward_varlen takes as k and v (a prefill over a cached
- * prefix); with H = Hkv it is the cache.  A value is lo + s c rounded to fp32, then
- * to o_dtype.  Invalid sequences are skipped and flagged as by
+ * prefix); with H = Hkv it is the cache.  A value is lo + s c rounded once to
+ * o_dtype.  Invalid sequences are skipped and flagged as by
  * fa_kvcache_append_quant (their rows are not written); a page outside
  * [0, num_pages) is flagged FA_ERR_PAGE and read as page 0.  Rows at or past
  * cu_seqlens[B] are not written.

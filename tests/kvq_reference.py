@@ -15,6 +15,17 @@ def round_bf16(x):
     return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(torch.bfloat16).float().numpy()
 
 
+def round_once(x, dtype):
+    """float64 x rounded once to bf16 or fp32, ties to even (results in the normal range or exact)."""
+    x = np.ascontiguousarray(x, dtype=np.float64)
+    if dtype == torch.float32:
+        return torch.from_numpy(x.astype(np.float32))
+    bits = x.view(np.uint64)
+    up = bits + np.uint64((1 << 44) - 1) + ((bits >> np.uint64(45)) & np.uint64(1))
+    y = np.where(np.isfinite(x), (up & ~np.uint64((1 << 45) - 1)).view(np.float64), x)
+    return torch.from_numpy(y.astype(np.float32)).to(torch.bfloat16)
+
+
 def quantise(x, bits):
     """codes uint8 [..., d], lo and s float32 [..., d / 32] of float32 x [..., d]."""
     g = np.asarray(x, np.float32).reshape(*x.shape[:-1], -1, GROUP)

@@ -89,7 +89,7 @@ def test_append_and_read_bit_for_bit(cuda_device, d, bits, Hkv, ps):
             got = fa.kvcache_read_quant(kp, vp, cu_of(rows, dev), i32(table, dev), i32(lens, dev), sum(rows), max(rows),
                                         3 * Hkv, d, bits, out_dtype=dt)
             for g, w in zip(got, want):
-                w = torch.from_numpy(np.repeat(w, 3, 1)).to(torch.float32).to(dt)
+                w = ref.round_once(np.repeat(w, 3, 1), dt)
                 assert torch.equal(g.cpu(), w)
     assert fa.fa_check_status() == fa.FA_OK
 
@@ -163,7 +163,7 @@ def test_append_and_read_invalid_sequences(cuda_device):
         for b in ok:
             n = cu[b + 1] - cu[b]
             w = ref.values(want, tab[b], range(lens[b] - n, lens[b]), d, bits, ref.K_UNIT)
-            assert torch.equal(ko[cu[b]:cu[b + 1]].cpu(), torch.from_numpy(w).float().to(torch.bfloat16))
+            assert torch.equal(ko[cu[b]:cu[b + 1]].cpu(), ref.round_once(w, torch.bfloat16))
 
     go([0, 4, 8, 12], [4, 30, 64], 4, fa.FA_OK, [])
     go([0, 4, 8, 10], [4, 30, 64], 4, fa.FA_OK, [])              # rows 10, 11 belong to nobody
@@ -199,7 +199,7 @@ def test_append_bad_page(cuda_device, bad):
     tab0 = np.where((table < 0) | (table >= 12), 0, table)  # read as page 0
     for b in range(3):
         w = ref.values(want, tab0[b], range(lens[b] - 20, lens[b]), d, bits, ref.K_UNIT)
-        assert torch.equal(got[cu[b]:cu[b + 1]].cpu(), torch.from_numpy(w).float().to(torch.bfloat16))
+        assert torch.equal(got[cu[b]:cu[b + 1]].cpu(), ref.round_once(w, torch.bfloat16))
 
 
 def check_decode(dev, q, kpool, vpool, table, lens, bits, scale, dtypes=(torch.float32, torch.bfloat16), kd=None, vd=None):
@@ -352,9 +352,9 @@ def test_pool_past_32_bits(cuda_device):
     small_k, small_v = kp[[pages - 1, pages - 3]].cpu().numpy(), vp[[pages - 1, pages - 3]].cpu().numpy()
     assert not kp[:pages - 3].any() and not kp[pages - 2].any()
     c, lo, s = ref.quantise(k.float().numpy(), bits)
-    want = torch.from_numpy(np.repeat(lo, 32, -1).astype(np.float64) + np.repeat(s, 32, -1).astype(np.float64) * c)
+    want = np.repeat(lo, 32, -1).astype(np.float64) + np.repeat(s, 32, -1).astype(np.float64) * c
     got, _ = fa.kvcache_read_quant(kp, vp, cu, table, lens, 100, 100, Hkv, d, bits)
-    assert torch.equal(got.cpu(), want.float().to(torch.bfloat16))
+    assert torch.equal(got.cpu(), ref.round_once(want, torch.bfloat16))
     q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(71)).to(torch.bfloat16)
     o_ref, lse_ref, tol_o, tol_l = ref.decode(q.double().numpy(), small_k, small_v, np.array([[0, 1]]), [100], bits, 0.1)
     o, lse = fa.decode_paged_quant(q.to(dev), kp, vp, table, lens, bits, scale=0.1)
@@ -384,8 +384,8 @@ def test_generation_over_a_quantised_cache(cuda_device):
         o, lse = fa.forward_varlen(q, k, v, cu_q, cu_k, max(new), scale=scale, causal=True)
         assert fa.fa_check_status() == fa.FA_OK
         kn, vn = kp.cpu().numpy(), vp.cpu().numpy()
-        kr, vr = (torch.from_numpy(np.repeat(np.concatenate([
-            ref.values(pool, table[b], range(lens[b]), d, bits, unit) for b in range(3)]), G, 1)).float().to(torch.bfloat16)
+        kr, vr = (ref.round_once(np.repeat(np.concatenate([
+            ref.values(pool, table[b], range(lens[b]), d, bits, unit) for b in range(3)]), G, 1), torch.bfloat16)
             for pool, unit in ((kn, ref.K_UNIT), (vn, ref.V_UNIT)))
         o_ref, lse_ref = oracle.forward_varlen(q.cpu(), kr, vr, cu_q.cpu().numpy(), cu_k.cpu().numpy(), scale, True)
         check_o(o, o_ref, "prefill over the read-back cache")
