@@ -983,8 +983,6 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.cap = max_blocks * page_size;
     // units are counted in int32, a little past the last one too; 16 keys is the shortest
     if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
-    // a page's bytes, in 16s, are counted in uint32
-    if (static_cast<long long>(Hkv) * page_size * kvq_row_bytes(d, bits) / 16 > 0xFFFFFFFFLL) return FA_ERR_INVALID_ARG;
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(H, Hkv, d)) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;

@@ -2,10 +2,10 @@
 // fa_kvcache_read_quant (declared in include/fa.h, format in kvquant.cuh).
 //
 // Both are one pass over the rows that they touch.  A block takes 16 tokens of one
-// sequence, all KV heads, K and V.  A warp takes 256 consecutive values of a token's
-// row at a time, K and V: a thread has 8 consecutive dimensions (16 bytes of bf16)
-// and always the same ones of a head, and the four threads of a 32-value group find
-// its least and largest value with two shuffles.
+// sequence, all KV heads, K and V, as one run of pieces dealt to its threads in order.
+// Appending, a thread has 16 consecutive values of K and of V (half a group: one shuffle
+// finds its least and greatest, and what is done once a group is done by two threads);
+// reading, 8, so that a warp's 16-byte stores are contiguous.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -61,13 +61,23 @@ __device__ __forceinline__ bool kvq_block(const KvqParams& p, int& b, int& first
     return n > 0;
 }
 
-// Page of each of the block's tokens, -1 where the table's entry is outside the pool.
-__device__ __forceinline__ void kvq_pages(const KvqParams& p, int b, int n, int pos0, int* s_page) {
+// Byte offset in a pool of each of the block's tokens' tile (KV head 0), or -1 where
+// the table's entry is outside the pool (read as page 0 if `clamp`).
+template <int D, int BITS>
+__device__ __forceinline__ void kvq_tiles(const KvqParams& p, int b, int n, int pos0, bool clamp, long long* s_tile) {
+    using F = KvqFormat<D, BITS>;
     if (threadIdx.x < n) {
-        const int pg = p.block_table[static_cast<size_t>(b) * p.max_blocks + ((pos0 + threadIdx.x) >> p.page_shift)];
+        const int pos = pos0 + threadIdx.x;
+        int pg = p.block_table[static_cast<size_t>(b) * p.max_blocks + (pos >> p.page_shift)];
         const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
-        if (!ok) atomicCAS(p.status, 0, FA_ERR_PAGE);
-        s_page[threadIdx.x] = ok ? pg : -1;
+        if (!ok) {
+            atomicCAS(p.status, 0, FA_ERR_PAGE);
+            pg = 0;
+        }
+        const int slot = pos & ((1 << p.page_shift) - 1);
+        const long long at = (static_cast<long long>(pg) * p.Hkv * F::kRowBytes << p.page_shift) +
+                             static_cast<long long>(slot / kKvqTile) * F::kTileBytes;
+        s_tile[threadIdx.x] = ok || clamp ? at : -1;
     }
     __syncthreads();
 }
@@ -80,55 +90,54 @@ __device__ __forceinline__ int kvq_code_off(int c, int u) {
     return plane * (kKvqTile * F::kPlaneBytes) + (u * F::kPlaneGroups + g) * (U * BITS / 8);
 }
 
-// The block's items: (token, 256 values of its row), dealt to the warps in turn.
-struct KvqItems {
-    int token, part, parts;
-    __device__ __forceinline__ KvqItems(int warp, int parts_) : token(0), part(warp), parts(parts_) { wrap(); }
-    __device__ __forceinline__ void wrap() {
-        while (part >= parts) part -= parts, ++token;
-    }
-    __device__ __forceinline__ void next() {
-        part += kKvqThreads / 32;
-        wrap();
-    }
-};
+// i / n for i < 16 n and n < 65536: the quotient's distance to the next integer, at
+// least 1 / (2 n), is far above the product's rounding.
+__device__ __forceinline__ int kvq_div(int i, float inv_n) { return __float2int_rz((static_cast<float>(i) + 0.5f) * inv_n); }
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
 __device__ __forceinline__ uint32_t as_word(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
-// Quantises the thread's 8 values.  Every thread of the warp takes part in the shuffles.
-// Each step of the format's definition is one fp32 operation rounded to nearest, so
-// none may be contracted into another.  An infinity or NaN anywhere in the group makes
-// hi - lo, and with it s, infinite or NaN (the minimum and maximum pass NaN on).
+// Quantises the thread's 16 values, half of a group whose other half the neighbouring
+// thread has: code[i] holds BITS * i / 4 bits and on.  Every thread of the warp takes
+// part in the shuffle.  Each step of the format's definition is one fp32 operation
+// rounded to nearest, so none may be contracted into another.  An infinity or NaN
+// anywhere in the group makes hi - lo, and with it s, infinite or NaN (the minimum and
+// maximum pass NaN on).
 template <int BITS>
-__device__ __forceinline__ void kvq_quantise(const uint4& raw, uint32_t (&code)[2], uint32_t& param) {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    __nv_bfloat162 lo2 = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
-    __nv_bfloat162 hi2 = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
-    // lo in the low half, hi in the high half, each over the thread's 8 values
+__device__ __forceinline__ void kvq_quantise(const uint32_t (&w)[8], uint32_t (&code)[BITS / 2], uint32_t& param) {
+    __nv_bfloat162 lo2 = as_bf162(w[0]), hi2 = lo2;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo2 = __hmin2_nan(lo2, as_bf162(w[i]));
+        hi2 = __hmax2_nan(hi2, as_bf162(w[i]));
+    }
     lo2 = __hmin2_nan(lo2, __lowhigh2highlow(lo2));
     hi2 = __hmax2_nan(hi2, __lowhigh2highlow(hi2));
-#pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(as_word(lo2), as_word(hi2), 0x7610), o);
-        lo2 = __hmin2_nan(lo2, as_bf162(other));  // low half
-        hi2 = __hmax2_nan(hi2, as_bf162(other));  // high half
-    }
+    // lo in the low half, hi in the high half
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, __byte_perm(as_word(lo2), as_word(hi2), 0x7610), 1);
+    lo2 = __hmin2_nan(lo2, as_bf162(other));  // low half
+    hi2 = __hmax2_nan(hi2, as_bf162(other));  // high half
     float lo = __uint_as_float(as_word(lo2) << 16);
     const float hi = __uint_as_float(as_word(hi2) & 0xFFFF0000u);
     constexpr float kMax = static_cast<float>((1 << BITS) - 1);
-    float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), kMax)));
-    if (!(s <= FLT_MAX)) {
-        s = 0.0f;
-        lo = __uint_as_float(0x7FC00000u);  // the group reads back as NaN
-    } else if (s < FLT_MIN) {
-        s = 0.0f;  // 1 / s would overflow
+    // (hi - lo) / kMax rounded to nearest, by Markstein's theorem: with y the nearest to 1 / kMax, the residual of
+    // q = d y is exact and one fused step rounds correctly (from d = kMax 2^-126 on, below which s is 0)
+    constexpr float y = 1.0f / kMax;
+    const float d = __fsub_rn(hi, lo), q = __fmul_rn(d, y);
+    float s = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-kMax, q, d), y, q)));
+    // 1 / s rounded to nearest: the approximation is within 2^-22, the step squares that, and 1 / s of an 8-bit s
+    // is a power of two or at least 2^-34 of itself away from where the rounding turns
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    float inv = fmaf(fmaf(-s, r, 1.0f), r, r);
+    uint32_t keep = 0xFFFFFFFFu;
+    if (!(s >= FLT_MIN && s <= FLT_MAX)) {  // below, 1 / s would overflow: the group stands for lo
+        if (!(s <= FLT_MAX)) lo = __uint_as_float(0x7FC00000u);  // it reads back as NaN
+        s = 0.0f, inv = 0.0f, keep = 0u;
     }
-    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    const uint32_t keep = s > 0.0f ? 0xFFFFFFFFu : 0u;
-    uint32_t c[8];
+    uint32_t c[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
         const float x = __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
         float t = __fmul_rn(__fsub_rn(x, lo), inv);
         // s is at least (1 - 2^-8) of the exact step: 15 / (1 - 2^-8) still rounds to 15, 255 / (1 - 2^-8) to 256
@@ -138,74 +147,94 @@ __device__ __forceinline__ void kvq_quantise(const uint4& raw, uint32_t (&code)[
     }
     constexpr uint32_t kMagic = 0x4B400000u;  // the bits of 2^23 + 2^22
     if constexpr (BITS == 4) {
-        uint32_t x = c[0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) x += c[i] << (4 * i);
-        code[0] = (x - kMagic * 0x11111111u) & keep;
-        code[1] = 0;
+        for (int j = 0; j < 2; ++j) {
+            uint32_t x = c[8 * j];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) x += c[8 * j + i] << (4 * i);
+            code[j] = (x - kMagic * 0x11111111u) & keep;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            code[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+        for (int j = 0; j < 4; ++j)
+            code[j] = __byte_perm(__byte_perm(c[4 * j], c[4 * j + 1], 0x0040), __byte_perm(c[4 * j + 2], c[4 * j + 3], 0x0040),
                                   0x5410) & keep;
     }
-    param = (__float_as_uint(lo) >> 16) | (__float_as_uint(s) & 0xFFFF0000u);
+    param = (__float_as_uint(lo) >> 16) | __float_as_uint(s);
 }
 
 template <int D, int BITS>
 __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) {
     using F = KvqFormat<D, BITS>;
-    __shared__ int s_page[kKvqTokens];
+    __shared__ long long s_tile[kKvqTokens];
     if (*p.status == FA_ERR_TIMEOUT) return;
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
-    kvq_pages(p, b, n, pos0, s_page);
-    constexpr int C = D / 8;       // threads of a head
-    constexpr int HW = 32 / C;     // heads of an item
-    const int lane = threadIdx.x & 31;
-    const int c = lane % C, u = c & 3, h0 = lane / C;
-    const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
-    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(c, u);
-    // V's units 2 u and 2 u + 1 of this group: of two neighbouring groups the even one writes unit 2 u of both,
-    // the odd one unit 2 u + 1
-    const bool odd = (c >> 2) & 1;
-    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>(c & ~4, 2 * u + odd);
-    const int p_off = F::kParamOff + (c >> 2) * 4;
-    for (KvqItems it(threadIdx.x >> 5, (p.Hkv + HW - 1) / HW); it.token < n; it.next()) {
-        const int i = it.token, h = it.part * HW + h0;
-        const bool live = h < p.Hkv;
-        const int at = (live ? h : 0) * D + c * 8;
-        const uint4 kr = __ldcs(reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + at));
-        const uint4 vr = __ldcs(reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + at));
-        uint32_t kc[2], vc[2], kp, vp;
-        kvq_quantise<BITS>(kr, kc, kp);
-        kvq_quantise<BITS>(vr, vc, vp);
-        uint32_t vw[2];  // V's word or words to write
-        if constexpr (BITS == 4) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, vc[0], 4);
-            vw[0] = odd ? __byte_perm(other, vc[0], 0x7632) : __byte_perm(vc[0], other, 0x5410);
-        } else {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vc[0] : vc[1], 4);
-            vw[0] = odd ? other : vc[0];
-            vw[1] = odd ? vc[1] : other;
+    kvq_tiles<D, BITS>(p, b, n, pos0, false, s_tile);
+    constexpr int C = D / 16;  // threads of a head
+    const int row = p.Hkv * C, total = n * row;
+    const float inv_row = 1.0f / static_cast<float>(row);
+    const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
+    // C divides the threads of a block: a thread always has the same dimensions of a head
+    const int c = threadIdx.x % C, half = c & 1;
+    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(2 * c, 2 * half);
+    constexpr int kUnitStepK = F::kPlaneGroups * kKvqUnitK * BITS / 8;  // from a unit to the next one of its group
+    constexpr int kUnitStepV = F::kPlaneGroups * kKvqUnitV * BITS / 8;
+    // V's units 4 half to 4 half + 3: of two neighbouring groups the even one writes the first two of both, the odd
+    // one the others, so that a store holds both groups' units
+    const bool odd = (c >> 1) & 1;
+    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>((2 * c) & ~4, 4 * half + 2 * odd);
+    const int p_off = F::kParamOff + (c >> 1) * 4;
+    for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
+        const int e = e0 + threadIdx.x;
+        const int at = min(e, total - C + c);  // the last head's, for threads past the end
+        const int i = kvq_div(at, inv_row), y = at - i * row;
+        uint32_t kw[8], vw[8];
+        {
+            const uint4* kf = reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + y * 16);
+            const uint4* vf = reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + y * 16);
+            const uint4 k0 = kf[0], k1 = kf[1], v0 = vf[0], v1 = vf[1];
+            kw[0] = k0.x, kw[1] = k0.y, kw[2] = k0.z, kw[3] = k0.w, kw[4] = k1.x, kw[5] = k1.y, kw[6] = k1.z, kw[7] = k1.w;
+            vw[0] = v0.x, vw[1] = v0.y, vw[2] = v0.z, vw[3] = v0.w, vw[4] = v1.x, vw[5] = v1.y, vw[6] = v1.z, vw[7] = v1.w;
         }
-        const int pg = s_page[i];
-        if (!live || pg < 0) continue;
-        const int slot = (pos0 + i) & ((1 << p.page_shift) - 1), r = slot % kKvqTile;
-        const size_t off = (static_cast<size_t>(pg) * p.Hkv + h) * block_bytes +
-                           static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
+        uint32_t kc[BITS / 2], vc[BITS / 2], kp, vp;
+        kvq_quantise<BITS>(kw, kc, kp);
+        kvq_quantise<BITS>(vw, vc, vp);
+        // of V: the two units to write, for both groups
+        uint32_t x[BITS / 2];
+        if constexpr (BITS == 4) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vc[0] : vc[1], 2);
+            const uint32_t even_g = odd ? other : vc[0], odd_g = odd ? vc[1] : other;
+            x[0] = __byte_perm(even_g, odd_g, 0x5410);
+            x[1] = __byte_perm(even_g, odd_g, 0x7632);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vc[j] : vc[2 + j], 2);
+                x[2 * j] = odd ? other : vc[j];
+                x[2 * j + 1] = odd ? vc[2 + j] : other;
+            }
+        }
+        const long long tile = s_tile[i];
+        if (e >= total || tile < 0) continue;
+        const int r = (pos0 + i) % kKvqTile;
+        const size_t off = tile + static_cast<uint64_t>(static_cast<uint32_t>(y / C)) * block_bytes;
         uint8_t* kt = p.kpages + off;
         uint8_t* vt = p.vpages + off;
         uint8_t* kd = kt + k_off + r * F::kPlaneBytes;
         uint8_t* vd = vt + v_off + r * F::kPlaneBytes;
         if constexpr (BITS == 4) {
             *reinterpret_cast<uint32_t*>(kd) = kc[0];
-            *reinterpret_cast<uint32_t*>(vd) = vw[0];
+            *reinterpret_cast<uint32_t*>(kd + kUnitStepK) = kc[1];
+            *reinterpret_cast<uint32_t*>(vd) = x[0];
+            *reinterpret_cast<uint32_t*>(vd + kUnitStepV) = x[1];
         } else {
             *reinterpret_cast<uint2*>(kd) = make_uint2(kc[0], kc[1]);
-            *reinterpret_cast<uint2*>(vd) = make_uint2(vw[0], vw[1]);
+            *reinterpret_cast<uint2*>(kd + kUnitStepK) = make_uint2(kc[2], kc[3]);
+            *reinterpret_cast<uint2*>(vd) = make_uint2(x[0], x[1]);
+            *reinterpret_cast<uint2*>(vd + kUnitStepV) = make_uint2(x[2], x[3]);
         }
-        if (u == 0) {
+        if (half == 0) {
             *reinterpret_cast<uint32_t*>(kt + p_off + r * F::kParamBytes) = kp;
             *reinterpret_cast<uint32_t*>(vt + p_off + r * F::kParamBytes) = vp;
         }
@@ -214,15 +243,15 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) 
 
 // The 8 values lo + s c of a chunk, each rounded once to the output type, written to the
 // G query heads that share the KV head.
-template <int D, int BITS>
-__device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t param, void* out, size_t at, int G, bool f32) {
-    if (f32) {
+template <int D, int BITS, bool F32>
+__device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t param, void* out, size_t at, int G) {
+    if constexpr (F32) {
         const float lo = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t c = BITS == 4 ? (code[0] >> (4 * i)) & 15u : (code[i >> 2] >> (8 * (i & 3))) & 255u;
-            x[i] = fmaf(s, static_cast<float>(c), lo);
+            x[i] = fmaf(s, __uint_as_float(0x4B000000u | c) - 8388608.0f, lo);
         }
         float* o = static_cast<float*>(out) + at;
         for (int g = 0; g < G; ++g, o += D) {
@@ -242,9 +271,8 @@ __device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t par
                 c = __hsub2(as_bf162(two), as_bf162(0x43004300u));
             } else {
                 // 2^23 + c in fp32; less 2^23, c fits the high half
-                const uint32_t w = code[i >> 1] >> (16 * (i & 1));
-                const float x0 = __uint_as_float(0x4B000000u | (w & 255u)) - 8388608.0f;
-                const float x1 = __uint_as_float(0x4B000000u | ((w >> 8) & 255u)) - 8388608.0f;
+                const float x0 = __uint_as_float(__byte_perm(code[i >> 1], 0x4B000000u, 0x7440 + 2 * (i & 1))) - 8388608.0f;
+                const float x1 = __uint_as_float(__byte_perm(code[i >> 1], 0x4B000000u, 0x7440 + 2 * (i & 1) + 1)) - 8388608.0f;
                 c = as_bf162(__byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632));
             }
             y[i] = as_word(__hfma2(s, c, lo));
@@ -254,50 +282,53 @@ __device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t par
     }
 }
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p, int f32) {
+template <int D, int BITS, bool F32>
+__global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p) {
     using F = KvqFormat<D, BITS>;
-    __shared__ int s_page[kKvqTokens];
+    __shared__ long long s_tile[kKvqTokens];
     if (*p.status == FA_ERR_TIMEOUT) return;
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
-    kvq_pages(p, b, n, pos0, s_page);
-    constexpr int C = D / 8, HW = 32 / C;
-    const int lane = threadIdx.x & 31;
-    const int c = lane % C, u = c & 3, h0 = lane / C;
-    const int G = p.H / p.Hkv;
-    const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
+    kvq_tiles<D, BITS>(p, b, n, pos0, true, s_tile);  // a bad entry is flagged and read as page 0
+    constexpr int C = D / 8;  // threads of a head
+    const int row = p.Hkv * C, total = n * row, G = p.H / p.Hkv;
+    const float inv_row = 1.0f / static_cast<float>(row);
+    const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
+    const int c = threadIdx.x % C, u = c & 3;
     const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(c, u);
-    const int v_off0 = kvq_code_off<D, BITS, kKvqUnitV>(c, 2 * u), v_off1 = kvq_code_off<D, BITS, kKvqUnitV>(c, 2 * u + 1);
+    // V's units 2 u and 2 u + 1: of two neighbouring groups the even one loads unit 2 u of both, the odd one the other
+    const bool odd = (c >> 2) & 1;
+    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>(c & ~4, 2 * u + odd);
     const int p_off = F::kParamOff + (c >> 2) * 4;
-    for (KvqItems it(threadIdx.x >> 5, (p.Hkv + HW - 1) / HW); it.token < n; it.next()) {
-        const int i = it.token, h = it.part * HW + h0;
-        if (h >= p.Hkv) continue;
-        const int pg = max(s_page[i], 0);  // a bad entry is flagged and read as page 0
-        const int slot = (pos0 + i) & ((1 << p.page_shift) - 1), r = slot % kKvqTile;
-        const size_t off = (static_cast<size_t>(pg) * p.Hkv + h) * block_bytes +
-                           static_cast<size_t>(slot / kKvqTile) * F::kTileBytes;
+    for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
+        const int e = e0 + threadIdx.x;
+        const int at = min(e, total - C + c);
+        const int i = kvq_div(at, inv_row), h = (at - i * row) / C;
+        const int r = (pos0 + i) % kKvqTile;
+        const size_t off = s_tile[i] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * block_bytes;
         const uint8_t* kt = p.kpages + off;
         const uint8_t* vt = p.vpages + off;
-        const uint8_t* kd = kt + k_off + r * F::kPlaneBytes;
-        const uint8_t* v0 = vt + v_off0 + r * F::kPlaneBytes;
-        const uint8_t* v1 = vt + v_off1 + r * F::kPlaneBytes;
-        uint32_t kc[2] = {0, 0}, vc[2] = {0, 0};
+        uint32_t kc[2], vc[2];
         if constexpr (BITS == 4) {
-            kc[0] = *reinterpret_cast<const uint32_t*>(kd);
-            vc[0] = *reinterpret_cast<const uint16_t*>(v0) |
-                    (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(v1)) << 16);
+            kc[0] = *reinterpret_cast<const uint32_t*>(kt + k_off + r * F::kPlaneBytes);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(vt + v_off + r * F::kPlaneBytes);  // (even, odd group)
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
+            vc[0] = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
+            kc[1] = vc[1] = 0;
         } else {
-            const uint2 k2 = *reinterpret_cast<const uint2*>(kd);
+            const uint2 k2 = *reinterpret_cast<const uint2*>(kt + k_off + r * F::kPlaneBytes);
+            const uint2 w = *reinterpret_cast<const uint2*>(vt + v_off + r * F::kPlaneBytes);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w.x : w.y, 4);
             kc[0] = k2.x, kc[1] = k2.y;
-            vc[0] = *reinterpret_cast<const uint32_t*>(v0);
-            vc[1] = *reinterpret_cast<const uint32_t*>(v1);
+            vc[0] = odd ? other : w.x;
+            vc[1] = odd ? w.y : other;
         }
         const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + p_off + r * F::kParamBytes);
         const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + p_off + r * F::kParamBytes);
-        const size_t at = (static_cast<size_t>(first + i) * p.H + h * G) * D + c * 8;
-        kvq_emit<D, BITS>(kc, kp, p.k_out, at, G, f32 != 0);
-        kvq_emit<D, BITS>(vc, vp, p.v_out, at, G, f32 != 0);
+        if (e >= total) continue;
+        const size_t to = (static_cast<size_t>(first + i) * p.H + h * G) * D + c * 8;
+        kvq_emit<D, BITS, F32>(kc, kp, p.k_out, to, G);
+        kvq_emit<D, BITS, F32>(vc, vp, p.v_out, to, G);
     }
 }
 
@@ -400,9 +431,11 @@ extern "C" int fa_kvcache_read_quant(const void* kpages, const void* vpages, con
     p.page_shift = kvq_page_shift(page_size);
     p.max_blocks = max_blocks;
     p.chunks = static_cast<int>(chunks);
-    const int f32 = o_dtype == FA_DT_F32;
     const cudaError_t e = by_format(d, bits, [&](auto D, auto BITS) {
-        fa_kvq_read<D(), BITS()><<<static_cast<unsigned>(B * chunks), kKvqThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, f32);
+        const unsigned grid = static_cast<unsigned>(B * chunks);
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        if (o_dtype == FA_DT_F32) fa_kvq_read<D(), BITS(), true><<<grid, kKvqThreads, 0, st>>>(p);
+        else fa_kvq_read<D(), BITS(), false><<<grid, kKvqThreads, 0, st>>>(p);
     });
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

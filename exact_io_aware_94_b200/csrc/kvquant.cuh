@@ -28,6 +28,7 @@ namespace fa {
 constexpr int kKvqGroup = 32;   // values that share lo and s
 constexpr int kKvqTile = 16;    // tokens of a tile; page sizes are multiples of it
 constexpr int kKvqUnitK = 8, kKvqUnitV = 4;
+constexpr int kKvqMaxHeads = 2048;  // KV heads: a row is 65,536 pieces of 8 at most, a page's bytes / 16 fit uint32
 
 template <int D, int BITS>
 struct KvqFormat {
@@ -51,6 +52,7 @@ inline int kvq_check_pool(int B, int H, int Hkv, int num_pages, int page_size, i
     if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
     if (bits != 4 && bits != 8) return FA_ERR_UNSUPPORTED;
     if (B <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || num_pages <= 0 || max_blocks <= 0) return FA_ERR_INVALID_ARG;
+    if (Hkv > kKvqMaxHeads) return FA_ERR_INVALID_ARG;
     if (page_size < kKvqTile || page_size > 65536 || (page_size & (page_size - 1)) != 0) return FA_ERR_INVALID_ARG;
     if (static_cast<long long>(max_blocks) * page_size > 0x7FFFFFFFLL || static_cast<long long>(B) * H > (1LL << 30) ||
         static_cast<long long>(B) * max_blocks > 0x7FFFFFFFLL)

@@ -254,7 +254,7 @@ int fa_decode_paged(const void* q, const void* kpages, const void* vpages, const
  *   - block_table int32 [B, max_blocks] and kv_lens int32 [B] as in
  *     fa_decode_paged.  kv_lens counts the positions valid AFTER an append, so an
  *     append, a read and a decode of one step take the same tensor.
- * d is 64, 128 or 256, bits 4 or 8.  Pools, q, k, v and outputs must be 16-byte
+ * d is 64, 128 or 256, bits 4 or 8, Hkv at most 2048.  Pools, q, k, v and outputs must be 16-byte
  * aligned, k and v strides multiples of 8 elements.
  */
 #define FA_KVQ_GROUP 32

@@ -29,6 +29,7 @@ POOL = [
     (dict(bits=16), fa.FA_ERR_UNSUPPORTED),
     (dict(B=0), fa.FA_ERR_INVALID_ARG),
     (dict(Hkv=0), fa.FA_ERR_INVALID_ARG),
+    (dict(H=4096, Hkv=4096), fa.FA_ERR_INVALID_ARG),
     (dict(pages=0), fa.FA_ERR_INVALID_ARG),
     (dict(blocks=0), fa.FA_ERR_INVALID_ARG),
     (dict(ps=8), fa.FA_ERR_INVALID_ARG),        # less than a tile

@@ -131,6 +131,33 @@ def test_append_unusual_values(cuda_device, bits):
     assert fa.fa_check_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_append_rounds_as_defined_at_every_exponent(cuda_device, bits):
+    """Groups of spreads from 2^-130 to 2^127 (quotient and reciprocal are computed without a division), and every
+    8-bit step: bit for bit."""
+    dev, d, ps = cuda_device, 128, 64
+    gen = torch.Generator().manual_seed(8)
+    n = 1024
+    x = torch.randn(n, 2, d, generator=gen, dtype=torch.float64)
+    x *= 2.0 ** torch.randint(-128, 124, (n, 2, d // 32, 1), generator=gen).expand(-1, -1, -1, 32).reshape(n, 2, d)
+    top = (torch.arange(128) / 128.0 + 1.0).repeat(n * 2 * (d // 32) // 128 // 2)  # every significand of hi, lo = 0
+    y = x.reshape(-1, 32)
+    y[: top.numel()] = y[: top.numel()].abs() / y[: top.numel()].abs().amax(1, keepdim=True)
+    y[: top.numel(), 0] = 0.0
+    y[: top.numel()] *= (top * (2 ** bits - 1) * 2.0 ** torch.randint(-60, 60, top.shape, generator=gen))[:, None]
+    x = y.reshape(n, 2, d).to(torch.bfloat16)
+    table = np.random.default_rng(2).permutation(n // ps)[None].astype(np.int32)
+    pool = np.zeros((n // ps, 2, ps * ref.row_bytes(d, bits)), np.uint8)
+    kpool, vpool = pool.copy(), pool.copy()
+    kp, vp = (torch.from_numpy(pool.copy()).to(dev) for _ in range(2))
+    f = x.float().numpy()
+    append_reference(kpool, vpool, f, f, [0, n], table, [n], bits)
+    fa.kvcache_append_quant(x.to(dev), x.to(dev), kp, vp, i32([0, n], dev), i32(table, dev), i32([n], dev), n, bits)
+    assert fa.fa_check_status() == fa.FA_OK
+    same_pool(kp.cpu().numpy(), kpool, d, bits)
+    same_pool(vp.cpu().numpy(), vpool, d, bits)
+
+
 def test_append_and_read_invalid_sequences(cuda_device):
     """Each invalid sequence or page is flagged and leaves the pools and the outputs as they were; its neighbours are
     served."""
