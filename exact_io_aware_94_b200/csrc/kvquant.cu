@@ -2,10 +2,9 @@
 // fa_kvcache_read_quant (declared in include/fa.h, format in kvquant.cuh).
 //
 // Both are one pass over the rows that they touch.  A block takes 16 tokens of one
-// sequence, all KV heads, K and V, as one run of pieces dealt to its threads in order.
-// Appending, a thread has 16 consecutive values of K and of V (half a group: one shuffle
-// finds its least and greatest, and what is done once a group is done by two threads);
-// reading, 8, so that a warp's 16-byte stores are contiguous.
+// sequence, all KV heads, K and V, as one run of pieces dealt to its threads in order:
+// 16 consecutive values of K and of V, half a group.  Two threads do what is done once
+// a group, and a piece of bf16 is one 32-byte sector.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,6 +14,7 @@
 
 #include "fa_internal.h"
 #include "kvquant.cuh"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
@@ -35,6 +35,7 @@ struct KvqParams {
     void* v_out;
     int* status;
     int B, H, Hkv, total, max_rows, num_pages, page_shift, max_blocks, chunks;
+    bool wide;               // read: k_out and v_out are 32-byte aligned
 };
 
 // What a block works on: rows [first, first + n) of the packed rows, which are the
@@ -163,45 +164,26 @@ __device__ __forceinline__ void kvq_quantise(const uint32_t (&w)[8], uint32_t (&
     param = (__float_as_uint(lo) >> 16) | __float_as_uint(s);
 }
 
+// Where a thread's pieces lie: D / 16 divides the threads of a block, so a thread always
+// has the same dimensions of a head.  Of V, it has units 4 half to 4 half + 3 of its
+// group; of two neighbouring groups the even one's thread stores (loads) the first two
+// of both, the odd one's the others, so that an access holds both groups' units.
 template <int D, int BITS>
-__global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) {
+struct KvqPiece {
     using F = KvqFormat<D, BITS>;
-    __shared__ long long s_tile[kKvqTokens];
-    if (*p.status == FA_ERR_TIMEOUT) return;
-    int b, first, n, pos0;
-    if (!kvq_block(p, b, first, n, pos0)) return;
-    kvq_tiles<D, BITS>(p, b, n, pos0, false, s_tile);
-    constexpr int C = D / 16;  // threads of a head
-    const int row = p.Hkv * C, total = n * row;
-    const float inv_row = 1.0f / static_cast<float>(row);
-    const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
-    // C divides the threads of a block: a thread always has the same dimensions of a head
-    const int c = threadIdx.x % C, half = c & 1;
-    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(2 * c, 2 * half);
-    constexpr int kUnitStepK = F::kPlaneGroups * kKvqUnitK * BITS / 8;  // from a unit to the next one of its group
-    constexpr int kUnitStepV = F::kPlaneGroups * kKvqUnitV * BITS / 8;
-    // V's units 4 half to 4 half + 3: of two neighbouring groups the even one writes the first two of both, the odd
-    // one the others, so that a store holds both groups' units
-    const bool odd = (c >> 1) & 1;
-    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>((2 * c) & ~4, 4 * half + 2 * odd);
-    const int p_off = F::kParamOff + (c >> 1) * 4;
-    for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
-        const int e = e0 + threadIdx.x;
-        const int at = min(e, total - C + c);  // the last head's, for threads past the end
-        const int i = kvq_div(at, inv_row), y = at - i * row;
-        uint32_t kw[8], vw[8];
-        {
-            const uint4* kf = reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + y * 16);
-            const uint4* vf = reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + y * 16);
-            const uint4 k0 = kf[0], k1 = kf[1], v0 = vf[0], v1 = vf[1];
-            kw[0] = k0.x, kw[1] = k0.y, kw[2] = k0.z, kw[3] = k0.w, kw[4] = k1.x, kw[5] = k1.y, kw[6] = k1.z, kw[7] = k1.w;
-            vw[0] = v0.x, vw[1] = v0.y, vw[2] = v0.z, vw[3] = v0.w, vw[4] = v1.x, vw[5] = v1.y, vw[6] = v1.z, vw[7] = v1.w;
-        }
-        uint32_t kc[BITS / 2], vc[BITS / 2], kp, vp;
-        kvq_quantise<BITS>(kw, kc, kp);
-        kvq_quantise<BITS>(vw, vc, vp);
-        // of V: the two units to write, for both groups
-        uint32_t x[BITS / 2];
+    static constexpr int kUnitStepK = F::kPlaneGroups * kKvqUnitK * BITS / 8;  // from a unit to the next one of its group
+    static constexpr int kUnitStepV = F::kPlaneGroups * kKvqUnitV * BITS / 8;
+    int c, k_off, v_off, p_off;
+    bool odd;
+    __device__ __forceinline__ explicit KvqPiece(int thread) {
+        c = thread % (D / 16);
+        odd = (c >> 1) & 1;
+        k_off = kvq_code_off<D, BITS, kKvqUnitK>(2 * c, 2 * (c & 1));
+        v_off = kvq_code_off<D, BITS, kKvqUnitV>((2 * c) & ~4, 4 * (c & 1) + 2 * odd);
+        p_off = F::kParamOff + (c >> 1) * 4;
+    }
+    // The piece's codes of V to the two units that the thread stores, and back.
+    __device__ __forceinline__ void to_stored(const uint32_t (&vc)[BITS / 2], uint32_t (&x)[BITS / 2]) const {
         if constexpr (BITS == 4) {
             const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? vc[0] : vc[1], 2);
             const uint32_t even_g = odd ? other : vc[0], odd_g = odd ? vc[1] : other;
@@ -215,70 +197,127 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) 
                 x[2 * j + 1] = odd ? vc[2 + j] : other;
             }
         }
+    }
+    __device__ __forceinline__ void from_stored(const uint32_t (&x)[BITS / 2], uint32_t (&vc)[BITS / 2]) const {
+        if constexpr (BITS == 4) {
+            const uint32_t even_g = __byte_perm(x[0], x[1], 0x5410), odd_g = __byte_perm(x[0], x[1], 0x7632);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? even_g : odd_g, 2);
+            vc[0] = odd ? other : even_g;
+            vc[1] = odd ? odd_g : other;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? x[2 * j] : x[2 * j + 1], 2);
+                vc[j] = odd ? other : x[2 * j];
+                vc[2 + j] = odd ? x[2 * j + 1] : other;
+            }
+        }
+    }
+};
+
+template <int D, int BITS>
+__global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) {
+    using F = KvqFormat<D, BITS>;
+    __shared__ long long s_tile[kKvqTokens];
+    if (*p.status == FA_ERR_TIMEOUT) return;
+    int b, first, n, pos0;
+    if (!kvq_block(p, b, first, n, pos0)) return;
+    kvq_tiles<D, BITS>(p, b, n, pos0, false, s_tile);
+    const KvqPiece<D, BITS> piece(threadIdx.x);
+    constexpr int C = D / 16;  // threads of a head
+    const int row = p.Hkv * C, total = n * row;
+    const float inv_row = 1.0f / static_cast<float>(row);
+    const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
+    for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
+        const int e = e0 + threadIdx.x;
+        const int at = min(e, total - C + piece.c);  // the last head's, for threads past the end
+        const int i = kvq_div(at, inv_row), y = at - i * row;
+        uint32_t kw[8], vw[8];
+        {
+            const uint4* kf = reinterpret_cast<const uint4*>(p.k + (first + i) * p.stride_k + y * 16);
+            const uint4* vf = reinterpret_cast<const uint4*>(p.v + (first + i) * p.stride_v + y * 16);
+            const uint4 k0 = kf[0], k1 = kf[1], v0 = vf[0], v1 = vf[1];
+            kw[0] = k0.x, kw[1] = k0.y, kw[2] = k0.z, kw[3] = k0.w, kw[4] = k1.x, kw[5] = k1.y, kw[6] = k1.z, kw[7] = k1.w;
+            vw[0] = v0.x, vw[1] = v0.y, vw[2] = v0.z, vw[3] = v0.w, vw[4] = v1.x, vw[5] = v1.y, vw[6] = v1.z, vw[7] = v1.w;
+        }
+        uint32_t kc[BITS / 2], vc[BITS / 2], kp, vp;
+        kvq_quantise<BITS>(kw, kc, kp);
+        kvq_quantise<BITS>(vw, vc, vp);
+        uint32_t x[BITS / 2];
+        piece.to_stored(vc, x);
         const long long tile = s_tile[i];
         if (e >= total || tile < 0) continue;
-        const int r = (pos0 + i) % kKvqTile;
-        const size_t off = tile + static_cast<uint64_t>(static_cast<uint32_t>(y / C)) * block_bytes;
+        const int r = static_cast<unsigned>(pos0 + i) % kKvqTile;
+        const size_t off = tile + static_cast<uint64_t>(static_cast<unsigned>(y) / C) * block_bytes;
         uint8_t* kt = p.kpages + off;
         uint8_t* vt = p.vpages + off;
-        uint8_t* kd = kt + k_off + r * F::kPlaneBytes;
-        uint8_t* vd = vt + v_off + r * F::kPlaneBytes;
+        uint8_t* kd = kt + piece.k_off + r * F::kPlaneBytes;
+        uint8_t* vd = vt + piece.v_off + r * F::kPlaneBytes;
         if constexpr (BITS == 4) {
             *reinterpret_cast<uint32_t*>(kd) = kc[0];
-            *reinterpret_cast<uint32_t*>(kd + kUnitStepK) = kc[1];
+            *reinterpret_cast<uint32_t*>(kd + piece.kUnitStepK) = kc[1];
             *reinterpret_cast<uint32_t*>(vd) = x[0];
-            *reinterpret_cast<uint32_t*>(vd + kUnitStepV) = x[1];
+            *reinterpret_cast<uint32_t*>(vd + piece.kUnitStepV) = x[1];
         } else {
             *reinterpret_cast<uint2*>(kd) = make_uint2(kc[0], kc[1]);
-            *reinterpret_cast<uint2*>(kd + kUnitStepK) = make_uint2(kc[2], kc[3]);
+            *reinterpret_cast<uint2*>(kd + piece.kUnitStepK) = make_uint2(kc[2], kc[3]);
             *reinterpret_cast<uint2*>(vd) = make_uint2(x[0], x[1]);
-            *reinterpret_cast<uint2*>(vd + kUnitStepV) = make_uint2(x[2], x[3]);
+            *reinterpret_cast<uint2*>(vd + piece.kUnitStepV) = make_uint2(x[2], x[3]);
         }
-        if (half == 0) {
-            *reinterpret_cast<uint32_t*>(kt + p_off + r * F::kParamBytes) = kp;
-            *reinterpret_cast<uint32_t*>(vt + p_off + r * F::kParamBytes) = vp;
+        if ((piece.c & 1) == 0) {
+            *reinterpret_cast<uint32_t*>(kt + piece.p_off + r * F::kParamBytes) = kp;
+            *reinterpret_cast<uint32_t*>(vt + piece.p_off + r * F::kParamBytes) = vp;
         }
     }
 }
 
-// The 8 values lo + s c of a chunk, each rounded once to the output type, written to the
+// The 16 values lo + s c of a piece, each rounded once to the output type, written to the
 // G query heads that share the KV head.
 template <int D, int BITS, bool F32>
-__device__ __forceinline__ void kvq_emit(const uint32_t (&code)[2], uint32_t param, void* out, size_t at, int G) {
+__device__ __forceinline__ void kvq_emit(const uint32_t (&code)[BITS / 2], uint32_t param, void* out, size_t at, int G,
+                                         bool wide) {
     if constexpr (F32) {
         const float lo = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
-        float x[8];
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t c = BITS == 4 ? (code[0] >> (4 * i)) & 15u : (code[i >> 2] >> (8 * (i & 3))) & 255u;
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t c = BITS == 4 ? (code[i / 8] >> (4 * (i % 8))) & 15u : (code[i / 4] >> (8 * (i % 4))) & 255u;
             x[i] = fmaf(s, __uint_as_float(0x4B000000u | c) - 8388608.0f, lo);
         }
         float* o = static_cast<float*>(out) + at;
-        for (int g = 0; g < G; ++g, o += D) {
-            *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
+        for (int g = 0; g < G; ++g, o += D)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(o + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     } else {
         const __nv_bfloat162 lo = as_bf162(__byte_perm(param, 0, 0x1010)), s = as_bf162(__byte_perm(param, 0, 0x3232));
-        uint32_t y[4];
+        uint32_t y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 8; ++i) {
             __nv_bfloat162 c;  // codes 2 i and 2 i + 1
             if constexpr (BITS == 4) {
                 // 0x4300 | c is 128 + c in bf16
-                const uint32_t up = i < 2 ? code[0] << (12 - 8 * i) : code[0] >> (8 * i - 12);
-                const uint32_t two = ((code[0] >> (8 * i)) & 0xFu) | (up & 0xF0000u) | 0x43004300u;
-                c = __hsub2(as_bf162(two), as_bf162(0x43004300u));
+                const uint32_t w = code[i / 4];
+                const int b = 8 * (i % 4);
+                const uint32_t up = b < 12 ? w << (12 - b) : w >> (b - 12);
+                c = __hsub2(as_bf162(((w >> b) & 0xFu) | (up & 0xF0000u) | 0x43004300u), as_bf162(0x43004300u));
             } else {
                 // 2^23 + c in fp32; less 2^23, c fits the high half
-                const float x0 = __uint_as_float(__byte_perm(code[i >> 1], 0x4B000000u, 0x7440 + 2 * (i & 1))) - 8388608.0f;
-                const float x1 = __uint_as_float(__byte_perm(code[i >> 1], 0x4B000000u, 0x7440 + 2 * (i & 1) + 1)) - 8388608.0f;
+                const uint32_t w = code[i / 2];
+                const float x0 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + 2 * (i & 1))) - 8388608.0f;
+                const float x1 = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + 2 * (i & 1) + 1)) - 8388608.0f;
                 c = as_bf162(__byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632));
             }
             y[i] = as_word(__hfma2(s, c, lo));
         }
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at;
-        for (int g = 0; g < G; ++g, o += D) *reinterpret_cast<uint4*>(o) = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int g = 0; g < G; ++g, o += D) {
+            if (wide) {  // 32-byte aligned outputs: whole sectors
+                st_global_v8(o, y);
+            } else {
+                *reinterpret_cast<uint4*>(o) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(o + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+        }
     }
 }
 
@@ -290,45 +329,41 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p) {
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
     kvq_tiles<D, BITS>(p, b, n, pos0, true, s_tile);  // a bad entry is flagged and read as page 0
-    constexpr int C = D / 8;  // threads of a head
+    const KvqPiece<D, BITS> piece(threadIdx.x);
+    constexpr int C = D / 16;
     const int row = p.Hkv * C, total = n * row, G = p.H / p.Hkv;
     const float inv_row = 1.0f / static_cast<float>(row);
     const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
-    const int c = threadIdx.x % C, u = c & 3;
-    const int k_off = kvq_code_off<D, BITS, kKvqUnitK>(c, u);
-    // V's units 2 u and 2 u + 1: of two neighbouring groups the even one loads unit 2 u of both, the odd one the other
-    const bool odd = (c >> 2) & 1;
-    const int v_off = kvq_code_off<D, BITS, kKvqUnitV>(c & ~4, 2 * u + odd);
-    const int p_off = F::kParamOff + (c >> 2) * 4;
+    const bool wide = p.wide;
     for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
         const int e = e0 + threadIdx.x;
-        const int at = min(e, total - C + c);
-        const int i = kvq_div(at, inv_row), h = (at - i * row) / C;
-        const int r = (pos0 + i) % kKvqTile;
+        const int at = min(e, total - C + piece.c);  // the last head's, for threads past the end
+        const int i = kvq_div(at, inv_row), h = static_cast<unsigned>(at - i * row) / C;
+        const int r = static_cast<unsigned>(pos0 + i) % kKvqTile;
         const size_t off = s_tile[i] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * block_bytes;
         const uint8_t* kt = p.kpages + off;
         const uint8_t* vt = p.vpages + off;
-        uint32_t kc[2], vc[2];
+        const uint8_t* kd = kt + piece.k_off + r * F::kPlaneBytes;
+        const uint8_t* vd = vt + piece.v_off + r * F::kPlaneBytes;
+        uint32_t kc[BITS / 2], vc[BITS / 2], x[BITS / 2];
         if constexpr (BITS == 4) {
-            kc[0] = *reinterpret_cast<const uint32_t*>(kt + k_off + r * F::kPlaneBytes);
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(vt + v_off + r * F::kPlaneBytes);  // (even, odd group)
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 4);
-            vc[0] = odd ? __byte_perm(other, w, 0x7632) : __byte_perm(w, other, 0x5410);
-            kc[1] = vc[1] = 0;
+            kc[0] = *reinterpret_cast<const uint32_t*>(kd);
+            kc[1] = *reinterpret_cast<const uint32_t*>(kd + piece.kUnitStepK);
+            x[0] = *reinterpret_cast<const uint32_t*>(vd);
+            x[1] = *reinterpret_cast<const uint32_t*>(vd + piece.kUnitStepV);
         } else {
-            const uint2 k2 = *reinterpret_cast<const uint2*>(kt + k_off + r * F::kPlaneBytes);
-            const uint2 w = *reinterpret_cast<const uint2*>(vt + v_off + r * F::kPlaneBytes);
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w.x : w.y, 4);
-            kc[0] = k2.x, kc[1] = k2.y;
-            vc[0] = odd ? other : w.x;
-            vc[1] = odd ? w.y : other;
+            const uint2 k0 = *reinterpret_cast<const uint2*>(kd), k1 = *reinterpret_cast<const uint2*>(kd + piece.kUnitStepK);
+            const uint2 v0 = *reinterpret_cast<const uint2*>(vd), v1 = *reinterpret_cast<const uint2*>(vd + piece.kUnitStepV);
+            kc[0] = k0.x, kc[1] = k0.y, kc[2] = k1.x, kc[3] = k1.y;
+            x[0] = v0.x, x[1] = v0.y, x[2] = v1.x, x[3] = v1.y;
         }
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + p_off + r * F::kParamBytes);
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + p_off + r * F::kParamBytes);
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + piece.p_off + r * F::kParamBytes);
+        const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + piece.p_off + r * F::kParamBytes);
+        piece.from_stored(x, vc);
         if (e >= total) continue;
-        const size_t to = (static_cast<size_t>(first + i) * p.H + h * G) * D + c * 8;
-        kvq_emit<D, BITS, F32>(kc, kp, p.k_out, to, G);
-        kvq_emit<D, BITS, F32>(vc, vp, p.v_out, to, G);
+        const size_t to = (static_cast<size_t>(first + i) * p.H + h * G) * D + piece.c * 16;
+        kvq_emit<D, BITS, F32>(kc, kp, p.k_out, to, G, wide);
+        kvq_emit<D, BITS, F32>(vc, vp, p.v_out, to, G, wide);
     }
 }
 
@@ -422,6 +457,7 @@ extern "C" int fa_kvcache_read_quant(const void* kpages, const void* vpages, con
     p.kv_lens = kv_lens;
     p.k_out = k_out;
     p.v_out = v_out;
+    p.wide = kvq_aligned(k_out, 32) && kvq_aligned(v_out, 32);
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;

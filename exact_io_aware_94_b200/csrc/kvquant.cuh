@@ -28,7 +28,7 @@ namespace fa {
 constexpr int kKvqGroup = 32;   // values that share lo and s
 constexpr int kKvqTile = 16;    // tokens of a tile; page sizes are multiples of it
 constexpr int kKvqUnitK = 8, kKvqUnitV = 4;
-constexpr int kKvqMaxHeads = 2048;  // KV heads: a row is 65,536 pieces of 8 at most, a page's bytes / 16 fit uint32
+constexpr int kKvqMaxHeads = 2048;  // KV heads: a row is 32,768 pieces of 16 at most, a page's bytes / 16 fit uint32
 
 template <int D, int BITS>
 struct KvqFormat {

@@ -203,6 +203,23 @@ def test_append_and_read_invalid_sequences(cuda_device):
     go([-2, 4, 8, 12], [9, 30, 64], 9, fa.FA_ERR_SEQLEN, [0])
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_read_into_outputs_aligned_to_16_bytes_only(cuda_device, bits):
+    dev, d, ps, Hkv, n = cuda_device, 64, 16, 3, 21
+    pool = ref.random_pool(2, Hkv, ps, d, bits, seed=7)
+    kp = torch.from_numpy(pool).to(dev)
+    out = torch.full((2, n * Hkv * d + 16), 5.0, dtype=torch.bfloat16, device=dev)
+    ko, vo = (o[8:8 + n * Hkv * d] for o in out)
+    assert ko.data_ptr() % 32 == 16
+    args = (i32([0, n], dev), i32([[1, 0]], dev), i32([n], dev))
+    assert fa.fa_kvcache_read_quant(kp, kp, *args, ko, vo, 1, Hkv, Hkv, n, n, 2, ps, 2, d, bits, fa.FA_DT_BF16) == fa.FA_OK
+    assert fa.fa_check_status() == fa.FA_OK
+    for o, unit in ((ko, ref.K_UNIT), (vo, ref.V_UNIT)):
+        w = ref.round_once(ref.values(pool, [1, 0], range(n), d, bits, unit), torch.bfloat16)
+        assert torch.equal(o.cpu().reshape(n, Hkv, d), w)
+    assert (out[:, :8] == 5.0).all() and (out[:, -8:] == 5.0).all()
+
+
 @pytest.mark.parametrize("bad", [-1, 12, 1 << 30])
 def test_append_bad_page(cuda_device, bad):
     dev, d, bits, ps, Hkv = cuda_device, 64, 4, 16, 2
