@@ -58,7 +58,9 @@ namespace {
 constexpr int kMaxSms = 160;        // bounds the CTAs of a launch and so the workspace
 constexpr int NC = 4;               // warps of a CTA
 constexpr int kThreads = 32 * NC;
-// CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone takes nt d / 4.
+// CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone
+// takes nt d / 4.  (One more with q in shared memory was no faster: 281 -> 289 us at d = 128, 48 -> 51 us at
+// d = 256.)
 __host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
 constexpr float kRefBits = 6.0f;    // u is 2^kRefBits at the running maximum
@@ -75,7 +77,6 @@ struct DecodeQuantParams {
     float* lse;
     int* status;
     float* part_o;    // [2 * CTAs][8 NT][D], normalised
-    float* part_w;    // [CTAs][warps][8 NT][D]: the part of the set that a warp's run starts inside of
     float* part_lse;  // [2 * CTAs][8 NT], base 2
     int4* first;      // [CTAs]: (sequence, head set, first unit, units) of the set that holds a CTA's first unit
     int2* plan;       // units of the batch, CTAs that share them
@@ -88,12 +89,17 @@ template <int D, int BITS, int NT>
 struct Cfg {
     using F = KvqFormat<D, BITS>;
     static constexpr int kCtas = ctas_per_sm(D, NT);
-    static constexpr int kRingBudget = (kCtas == 4 ? 46 : kCtas == 3 ? 62 : 84) * 1024;  // of a CTA
-    static constexpr int kBlocks = 8 * F::kTileBytes * NC <= kRingBudget ? 2 : 1;  // tiles of a unit
+    static constexpr int kBudget = 228 * 1024 / kCtas - 1024;    // of a CTA
+    static constexpr int kFixed = NC * 8 * NT * D * 4 + 512;     // the warps' first parts
+    // a warp's scores, parameters and stages of a unit of n tiles
+    static constexpr int per_warp(int n, int stages) {
+        return 8 * NT * (16 * n + 4) * 4 + n * F::kGroups * 64 + 8 * NT * 8 + 64 + stages * 2 * n * F::kTileBytes;
+    }
+    static constexpr int kBlocks = kFixed + NC * per_warp(2, 2) <= kBudget ? 2 : 1;  // tiles of a unit
+    static constexpr int S = kFixed + NC * per_warp(kBlocks, 4) <= kBudget ? 4 : kFixed + NC * per_warp(kBlocks, 3) <= kBudget ? 3 : 2;
     static constexpr int KT = 16 * kBlocks;
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kHalf;
-    static constexpr int S = kRingBudget / (kStageBytes * NC) < 4 ? kRingBudget / (kStageBytes * NC) : 4;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
     // V's s and lo of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], lo [tile][group][key % 4][key / 4]
@@ -108,7 +114,8 @@ struct Cfg {
     static constexpr int kRingOff = 0;
     static constexpr int kScoreOff = kRingOff + NC * kRingBytes;
     static constexpr int kParOff = kScoreOff + NC * kScoreBytes;
-    static constexpr int kMetaOff = kParOff + NC * kParBytes;          // [warp][first, last part] of Part
+    static constexpr int kFirstOff = kParOff + NC * kParBytes;         // [warp][head][D]
+    static constexpr int kMetaOff = kFirstOff + NC * HP * D * 4;       // [warp][first, last part] of Part
     static constexpr int kLseOff = kMetaOff + NC * 2 * 32;             // [warp][first, last part][head], base 2
     static constexpr int kMiscOff = kLseOff + NC * 2 * HP * 4;
     static constexpr int kBytes = kMiscOff + 32 * 4;
@@ -368,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     auto pair_key = [&](int i) { return (pair_of(i) / 2) % 4 + 8 * (pair_of(i) % 2); };
     float* sc = reinterpret_cast<float*>(smem + C::kScoreOff + warp * C::kScoreBytes);  // [head][key]: scores
     uint8_t* par = smem + C::kParOff + warp * C::kParBytes;
+    auto first_part = [&](int w) { return reinterpret_cast<float*>(smem + C::kFirstOff) + w * HP * D; };
     int s = 0;
     for (int at = w0; at < w1;) {
         cur.seek(p, at);
@@ -427,17 +435,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     sum += f[i];
                     f[i] *= up;
                 }
-                if constexpr (BITS == 4) {
-                    qb[nt][g][0] = pack_f16x2(f[0], f[4]);
-                    qb[nt][g][1] = pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f);
-                    qb[nt][g][2] = pack_f16x2(f[2], f[6]);
-                    qb[nt][g][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
-                } else {
-                    qb[nt][g][0] = pack_f16x2(f[0], f[2]);
-                    qb[nt][g][1] = pack_f16x2(f[1], f[3]);
-                    qb[nt][g][2] = pack_f16x2(f[4], f[6]);
-                    qb[nt][g][3] = pack_f16x2(f[5], f[7]);
-                }
+                uint4 b;
+                if constexpr (BITS == 4)
+                    b = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1] * 0.0625f, f[5] * 0.0625f), pack_f16x2(f[2], f[6]),
+                                   pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f));
+                else
+                    b = make_uint4(pack_f16x2(f[0], f[2]), pack_f16x2(f[1], f[3]), pack_f16x2(f[4], f[6]), pack_f16x2(f[5], f[7]));
+                qb[nt][g][0] = b.x, qb[nt][g][1] = b.y, qb[nt][g][2] = b.z, qb[nt][g][3] = b.w;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum *= p.scale_log2;
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         // heads 2 t, 2 t + 1
         const bool before = at > cur.begin, after = end < cur.begin + cur.n;
         const bool whole = !before && !after;
-        float* part = before ? p.part_w + (static_cast<size_t>(cta) * NC + warp) * HP * D : reinterpret_cast<float*>(ring);
+        float* part = before ? first_part(warp) : reinterpret_cast<float*>(ring);
         __syncwarp();  // the ring has been read
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         if (first.kind) {
             if (n_from == 0) before = true;  // only warp 0's: the set starts before the CTA
             of = first;
-            from[n_from] = p.part_w + (static_cast<size_t>(cta) * NC + w) * HP * D;
+            from[n_from] = first_part(w);
             from_lse[n_from++] = part_lse + 2 * w * HP;
             if (first.kind == 1) merge(false);
         }
@@ -947,11 +951,18 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
 int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-size_t part_bytes(int d, int nt) { return up256(static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * (d + 1) * sizeof(float)); }
-size_t warp_part_bytes(int d, int nt) { return up256(static_cast<size_t>(max_ctas(d, nt)) * NC * 8 * nt * d * sizeof(float)); }
-size_t workspace_bytes_of(int H, int Hkv, int d) {
+struct Workspace {
+    size_t lse, first, plan, total;  // offsets of the arrays after part_o
+};
+Workspace workspace_of(int H, int Hkv, int d) {
     const int nt = tiles_of(H / Hkv, d);
-    return part_bytes(d, nt) + warp_part_bytes(d, nt) + up256(max_ctas(d, nt) * sizeof(int4)) + 256;
+    const size_t ctas = max_ctas(d, nt), heads = 8 * nt;
+    Workspace w{};
+    w.lse = up256(2 * ctas * heads * d * sizeof(float));
+    w.first = w.lse + up256(2 * ctas * heads * sizeof(float));
+    w.plan = w.first + up256(ctas * sizeof(int4));
+    w.total = w.plan + 256;
+    return w;
 }
 
 }  // namespace
@@ -962,7 +973,7 @@ using namespace fa;
 
 extern "C" size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits) {
     if (kvq_check_pool(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
-    return workspace_bytes_of(H, Hkv, d);
+    return workspace_of(H, Hkv, d).total;
 }
 
 extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
@@ -983,7 +994,8 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.cap = max_blocks * page_size;
     // units are counted in int32, a little past the last one too; 16 keys is the shortest
     if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
-    if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < workspace_bytes_of(H, Hkv, d)) return FA_ERR_WORKSPACE;
+    const Workspace at = workspace_of(H, Hkv, d);
+    if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < at.total) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -998,12 +1010,9 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.lse = lse;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
-    p.part_lse = p.part_o + static_cast<size_t>(2 * max_ctas(d, nt)) * 8 * nt * d;
-    ws += part_bytes(d, nt);
-    p.part_w = reinterpret_cast<float*>(ws);
-    ws += warp_part_bytes(d, nt);
-    p.first = reinterpret_cast<int4*>(ws);
-    p.plan = reinterpret_cast<int2*>(ws + up256(max_ctas(d, nt) * sizeof(int4)));
+    p.part_lse = reinterpret_cast<float*>(ws + at.lse);
+    p.first = reinterpret_cast<int4*>(ws + at.first);
+    p.plan = reinterpret_cast<int2*>(ws + at.plan);
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
