@@ -78,8 +78,8 @@ struct DecodeQuantParams {
     int* status;
     float* part_o;    // [2 * CTAs][8 NT][D], normalised
     float* part_lse;  // [2 * CTAs][8 NT], base 2
-    int4* first;      // [CTAs]: (sequence, head set, first unit, units) of the set that holds a CTA's first unit
-    int2* plan;       // units of the batch, CTAs that share them
+    int4* cut;        // [CTAs]: the set that is cut at a CTA's first unit: (first row of o, heads, first CTA of it, CTAs); or 0 CTAs
+    int* used;        // CTAs that have units
     int B, H, Hkv, num_pages, page_shift, max_blocks, cap, sets;  // sets: head sets of a KV head
     float scale, scale_log2;
     int o_dtype;
@@ -189,6 +189,10 @@ __device__ __forceinline__ int units_of(int len) {
 }
 __device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
 
+// floor(a / b) for 0 <= a < 2^42 and 0 < b < 2^31 with a quotient below 2^31 where b < 2^10, below 2^10 otherwise: the
+// quotient is at least 1 / b below the next integer, far more than its rounding to 53 bits.
+__device__ __forceinline__ int div_floor(long long a, int b) { return static_cast<int>(static_cast<double>(a) / static_cast<double>(b)); }
+
 // A place in the batch's order of units: the set that unit v belongs to.
 template <int KT>
 struct Cursor {
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     // a CTA has a unit for each of its compute warps before another one is used
     const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / NC));
     const int cta = blockIdx.x;
-    if (cta == 0 && tid == 0) *p.plan = make_int2(U, n_cta);
+    if (cta == 0 && tid == 0) *p.used = n_cta;
     if (cta >= n_cta) return;
     // sequences without keys
     for (int b = cta; b < p.B; b += n_cta) {
@@ -280,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         for (int i = tid; i < p.H; i += kThreads) p.lse[static_cast<size_t>(b) * p.H + i] = -INFINITY;
     }
     if (U == 0) return;
-    const int u0 = static_cast<int>(static_cast<long long>(U) * cta / n_cta);
-    const int u1 = static_cast<int>(static_cast<long long>(U) * (cta + 1) / n_cta);
+    const int u0 = div_floor(static_cast<long long>(U) * cta, n_cta);
+    const int u1 = div_floor(static_cast<long long>(U) * (cta + 1), n_cta);
     {
         // the thread whose sequences hold unit u0
         const int lo = (incl - mine) * HH, hi = incl * HH;
@@ -292,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 if (u0 < at + n * HH) {
                     const int hh = (u0 - at) / n;
                     misc[1] = b, misc[2] = hh, misc[3] = at + hh * n, misc[4] = len;
-                    p.first[cta] = make_int4(b, hh, at + hh * n, n);
                     break;
                 }
                 at += n * HH;
@@ -754,6 +757,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         at = end;
     }
 
+    if (tid == 0) {
+        // for the combine kernel: the set of the CTA's first unit, if that is not the set's first one too
+        const int b = misc[1], hkv = misc[2] / p.sets, h_in = (misc[2] - hkv * p.sets) * HP, begin = misc[3];
+        const int c0 = div_floor((begin + 1LL) * n_cta - 1, U);
+        const int c1 = div_floor((begin + static_cast<long long>(units_of<KT>(misc[4]))) * n_cta - 1, U);
+        p.cut[cta] = make_int4(b * p.H + hkv * group + h_in, min(HP, group - h_in), c0, begin == u0 ? 0 : c1 - c0 + 1);
+    }
+
     // ---- the CTA's parts: those of one set are neighbours in the order first, last of warp 0, first, last of warp 1, ...
     __syncthreads();
     const float* from[NC];
@@ -817,65 +828,79 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 }
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
-// CTAs has P - 1 such blocks, each of which merges a share of its outputs: a warp finds
-// the P weights of a head, then the block's threads share the outputs and the parts.
-constexpr int kCombineThreads = 128;
+// CTAs has P - 1 such blocks, each of which merges a share of its outputs, four at a time.  What bounds it
+// is the latency of its loads, so all that a thread needs is asked for at once: 6 us with the loads in turn, 2 us so.
+constexpr int kCombineThreads = 256;
 template <int D, int NT>
 __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
-    constexpr int HP = 8 * NT;
+    constexpr int HP = 8 * NT, D4 = D / 4;
     __shared__ float s_w[HP][max_ctas(D, NT)];  // of part c0 + i, normalised
-    __shared__ float s_o[kCombineThreads];
+    __shared__ float4 s_o[kCombineThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel has ended and its writes are visible
     const int status = *static_cast<volatile const int*>(p.status);
-    const int2 plan = *p.plan;
-    const int4 set = p.first[i];  // sequence, set, first unit, units
-    if (status == FA_ERR_TIMEOUT || i >= plan.y) return;
-    const long long U = plan.x, n_cta = plan.y;
-    if (set.z == static_cast<int>(U * i / n_cta)) return;  // starts with the CTA
-    const int c0 = static_cast<int>(((set.z + 1LL) * n_cta - 1) / U);
-    const int P = static_cast<int>((static_cast<long long>(set.z + set.w) * n_cta - 1) / U) - c0 + 1;
-    const int hkv = set.y / p.sets, group = p.H / p.Hkv, h_in = (set.y - hkv * p.sets) * HP;
-    const int G = min(HP, group - h_in);
-    const size_t head0 = static_cast<size_t>(set.x) * p.H + hkv * group + h_in;
-    // outputs e0 to e1 of the set's G D
-    const int share = (G * D + P - 2) / (P - 1);
-    const int e0 = (i - c0 - 1) * share, e1 = min(G * D, e0 + share);
+    const int used = *p.used;
+    const int4 cut = p.cut[i];
+    if (status == FA_ERR_TIMEOUT || i >= used || cut.w == 0) return;
+    const size_t head0 = cut.x;
+    const int G = cut.y, c0 = cut.z, P = cut.w;
+    // outputs 4 e0 to 4 e1 of the set's G D
+    const int share = (G * D4 + P - 2) / (P - 1);
+    const int e0 = (i - c0 - 1) * share, e1 = min(G * D4, e0 + share);
     if (e0 >= e1) return;
-    // part i is the last one CTA c0 wrote (slot 2 c0 + 1), or the first one of a later CTA
+    // part c is the last one CTA c0 wrote (slot 2 c0 + 1), or the first one of a later CTA
     auto slot = [&](int c) { return static_cast<size_t>(2 * (c0 + c) + (c == 0)) * HP; };
-    auto store = [&](int e, float x) {
-        const size_t at = (head0 + e / D) * D + e % D;
-        if (p.o_dtype == FA_DT_F32) static_cast<float*>(p.o)[at] = x;
-        else static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(x);
+    auto part = [&](int c, int e) { return *reinterpret_cast<const float4*>(p.part_o + slot(c) * D + 4 * e); };
+    auto add = [](float4& o, float w, const float4& y) {
+        o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
+    };
+    auto store = [&](int e, const float4& x) {
+        const size_t at = head0 * D + 4 * e;
+        if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = x;
+        else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     };
     constexpr int kFew = 6;
-    if (P <= kFew) {  // a thread an output, all its loads at once
+    if (P <= kFew) {  // a thread four outputs
         for (int e = e0 + tid; e < e1; e += kCombineThreads) {
-            const int h = e / D, d = e % D;
-            float x[kFew], y[kFew], M = -INFINITY;
+            const int h = e / D4;
+            float x[kFew], M = -INFINITY;
+            float4 y[kFew];
 #pragma unroll
             for (int c = 0; c < kFew; ++c) {
                 x[c] = c < P ? p.part_lse[slot(c) + h] : -INFINITY;
-                y[c] = c < P ? p.part_o[(slot(c) + h) * D + d] : 0.0f;
+                y[c] = c < P ? part(c, e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll
             for (int c = 0; c < kFew; ++c) M = fmaxf(M, x[c]);
-            float L = 0.0f, O = 0.0f;
+            float L = 0.0f;
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int c = 0; c < kFew; ++c) {
                 if (c >= P) break;
                 const float w = x[c] == M ? 1.0f : ex2_approx(x[c] - M);
                 L += w;
-                O = fmaf(w, y[c], O);
+                add(O, w, y[c]);
             }
-            store(e, O / L);
-            if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+            store(e, make_float4(O.x / L, O.y / L, O.z / L, O.w / L));
+            if (e % D4 == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
         }
         return;
     }
-    for (int h = e0 / D + warp; h <= (e1 - 1) / D; h += kCombineThreads / 32) {
+    // W columns of four outputs, kCombineThreads / W threads each; a thread's first kAhead parts are asked for
+    // before the weights are known
+    constexpr int kAhead = 4;
+    int W = kCombineThreads / 2;
+    while (W > 4 && W / 2 >= share) W /= 2;
+    const int col = tid % W, row = tid / W, rows = kCombineThreads / W;
+    float4 ahead[kAhead];
+    {
+        const int e = min(e0 + col, e1 - 1);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (row + k * rows < P) ahead[k] = part(row + k * rows, e);
+    }
+    for (int h = e0 / D4 + warp; h <= (e1 - 1) / D4; h += kCombineThreads / 32) {
         float M = -INFINITY;
         for (int c = lane; c < P; c += 32) {
             s_w[h][c] = p.part_lse[slot(c) + h];
@@ -892,28 +917,27 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
 #pragma unroll
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         for (int c = lane; c < P; c += 32) s_w[h][c] /= L;
-        if (lane == 0 && h * D >= e0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+        if (lane == 0 && h * D4 >= e0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
     }
     __syncthreads();
-    // W columns of outputs, kCombineThreads / W threads each
-    int W = kCombineThreads;
-    while (W > 4 && W / 2 >= share) W /= 2;
-    const int col = tid % W, row = tid / W, rows = kCombineThreads / W;
     for (int eb = e0; eb < e1; eb += W) {
-        const int e = min(eb + col, e1 - 1), h = e / D, d = e % D;
-        float x = 0.0f;
-#pragma unroll 8
-        for (int c = row; c < P; c += rows) x = fmaf(s_w[h][c], p.part_o[(slot(c) + h) * D + d], x);
-        if (rows > 1) {
-            s_o[tid] = x;
-            __syncthreads();
-            for (int k = rows / 2; k > 0; k /= 2) {
-                if (row < k) s_o[tid] += s_o[tid + k * W];
-                __syncthreads();
-            }
-            x = s_o[col];
+        const int e = min(eb + col, e1 - 1), h = e / D4;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        int c = row;
+        if (eb == e0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k, c += rows)
+                if (c < P) add(x, s_w[h][c], ahead[k]);
         }
-        if (row == 0 && eb + col < e1) store(e, x);
+#pragma unroll 4
+        for (; c < P; c += rows) add(x, s_w[h][c], part(c, e));
+        s_o[tid] = x;
+        __syncthreads();
+        for (int k = rows / 2; k > 0; k /= 2) {
+            if (row < k) add(s_o[tid], 1.0f, s_o[tid + k * W]);
+            __syncthreads();
+        }
+        if (row == 0 && eb + col < e1) store(e, s_o[col]);
         __syncthreads();
     }
 }
@@ -952,16 +976,16 @@ int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct Workspace {
-    size_t lse, first, plan, total;  // offsets of the arrays after part_o
+    size_t lse, cut, used, total;  // offsets of the arrays after part_o
 };
 Workspace workspace_of(int H, int Hkv, int d) {
     const int nt = tiles_of(H / Hkv, d);
     const size_t ctas = max_ctas(d, nt), heads = 8 * nt;
     Workspace w{};
     w.lse = up256(2 * ctas * heads * d * sizeof(float));
-    w.first = w.lse + up256(2 * ctas * heads * sizeof(float));
-    w.plan = w.first + up256(ctas * sizeof(int4));
-    w.total = w.plan + 256;
+    w.cut = w.lse + up256(2 * ctas * heads * sizeof(float));
+    w.used = w.cut + up256(ctas * sizeof(int4));
+    w.total = w.used + 256;
     return w;
 }
 
@@ -1011,8 +1035,8 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_lse = reinterpret_cast<float*>(ws + at.lse);
-    p.first = reinterpret_cast<int4*>(ws + at.first);
-    p.plan = reinterpret_cast<int2*>(ws + at.plan);
+    p.cut = reinterpret_cast<int4*>(ws + at.cut);
+    p.used = reinterpret_cast<int*>(ws + at.used);
     p.B = B;
     p.H = H;
     p.Hkv = Hkv;
