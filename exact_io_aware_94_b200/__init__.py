@@ -415,20 +415,39 @@ def _kvq_device(t, name):
     return t.get_device()
 
 
-def _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits):
-    """(page size, sequences, table width) of a pair of pools and their table, checked."""
-    _kvq_check(dev, (kpages, "kpages", torch.uint8), (vpages, "vpages", torch.uint8),
-               (block_table, "block_table", torch.int32), (kv_lens, "kv_lens", torch.int32))
-    if kpages.dim() != 3 or kpages.shape != vpages.shape:
+# bytes of a token and KV head: codes, then (lo, s) of each group
+_KVQ_ROW = {(d, bits): d * bits // 8 + d // KVQ_GROUP * 4 for d in (64, 128, 256) for bits in (4, 8)}
+
+
+def _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits, cu=None):
+    """(num_pages, KV heads, page size, sequences, table width) of a pair of pools and their table, checked."""
+    try:  # what follows repeats the checks of the slow path, without its names
+        fine = (kpages.dtype is torch.uint8 and vpages.dtype is torch.uint8 and block_table.dtype is torch.int32
+                and kv_lens.dtype is torch.int32 and kpages.get_device() == dev and vpages.get_device() == dev
+                and block_table.get_device() == dev and kv_lens.get_device() == dev and kpages.is_contiguous()
+                and vpages.is_contiguous() and block_table.is_contiguous() and kv_lens.is_contiguous()
+                and (cu is None or (cu.dtype is torch.int32 and cu.get_device() == dev and cu.is_contiguous())))
+    except AttributeError:
+        fine = False
+    if not fine:
+        _kvq_check(dev, (kpages, "kpages", torch.uint8), (vpages, "vpages", torch.uint8),
+                   (block_table, "block_table", torch.int32), (kv_lens, "kv_lens", torch.int32))
+        if cu is not None:
+            _kvq_check(dev, (cu, "cu_seqlens", torch.int32))
+    shape, table = kpages.shape, block_table.shape
+    if len(shape) != 3 or shape != vpages.shape:
         raise ValueError("kpages and vpages must both be [num_pages, Hkv, page_bytes]")
-    if block_table.dim() != 2 or kv_lens.dim() != 1 or kv_lens.shape[0] != block_table.shape[0]:
+    if len(table) != 2 or kv_lens.shape != table[:1]:
         raise ValueError("block_table must be [B, max_blocks] and kv_lens [B]")
-    if d not in (64, 128, 256) or bits not in (4, 8):
+    if cu is not None and cu.shape != (table[0] + 1,):
+        raise ValueError("cu_seqlens must be [B + 1]")
+    row = _KVQ_ROW.get((d, bits))
+    if row is None:
         raise FAError(FA_ERR_UNSUPPORTED, "quantised cache with d = %r, bits = %r" % (d, bits))
-    page_size, rest = divmod(kpages.shape[2], d * bits // 8 + d // KVQ_GROUP * 4)
+    page_size, rest = divmod(shape[2], row)
     if rest or page_size == 0:
-        raise ValueError("a page of %d bytes is not whole tokens of d = %d in %d bits" % (kpages.shape[2], d, bits))
-    return (page_size,) + tuple(block_table.shape)
+        raise ValueError("a page of %d bytes is not whole tokens of d = %d in %d bits" % (shape[2], d, bits))
+    return shape[0], shape[1], page_size, table[0], table[1]
 
 
 def _kvq_run(dev, stream, call):
@@ -458,27 +477,26 @@ def kvcache_append_quant(k, v, kpages, vpages, cu_seqlens_new, block_table, kv_l
     positions of each sequence: rows [cu_seqlens_new[b], cu_seqlens_new[b+1]) become positions up to kv_lens[b] (the
     length after the append).  cu_seqlens_new int32 [B+1], block_table int32 [B,max_blocks], kv_lens int32 [B]."""
     dev = _kvq_device(k, "k")
-    strides = []
-    for t, n in ((k, "k"), (v, "v")):
-        if _kvq_device(t, n) != dev or t.dtype != torch.bfloat16 or t.dim() != 3:
-            raise ValueError("%s must be a bfloat16 tensor [total_new, Hkv, d] on device %d" % (n, dev))
-        T, Hkv, d = t.shape
-        s = t.stride()
-        if (d > 1 and s[2] != 1) or (Hkv > 1 and s[1] != d):
-            raise ValueError("the heads of a row of %s must be contiguous" % n)
-        strides.append(s[0] if T > 1 else Hkv * d)
-    if k.shape != v.shape:
-        raise ValueError("k and v must have the same shape")
-    page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
-    _kvq_check(dev, (cu_seqlens_new, "cu_seqlens_new", torch.int32))
-    if cu_seqlens_new.shape != (B + 1,) or kpages.shape[1] != Hkv:
-        raise ValueError("cu_seqlens_new must be [B + 1] and the pools' KV heads k's")
+    if _kvq_device(v, "v") != dev or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+        raise ValueError("k and v must be bfloat16 tensors on one device")
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape:
+        raise ValueError("k and v must both be [total_new, Hkv, d]")
+    T, Hkv, d = shape
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1 or (Hkv > 1 and (ks[1] != d or vs[1] != d)):
+        raise ValueError("the heads of a row of k and v must be contiguous")
+    num_pages, heads, page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits,
+                                                            cu_seqlens_new)
+    if heads != Hkv:
+        raise ValueError("the pools have %d KV heads, k and v %d" % (heads, Hkv))
     if T == 0:
         return
-    _check(_kvq_run(dev, stream, lambda handle: load_library().fa_kvcache_append_quant(
-        k.data_ptr(), v.data_ptr(), strides[0], strides[1], kpages.data_ptr(), vpages.data_ptr(),
-        cu_seqlens_new.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), B, Hkv, T, int(max_seqlen_new),
-        kpages.shape[0], page_size, max_blocks, d, bits, handle)), "fa_kvcache_append_quant")
+    dense = Hkv * d  # the stride of a single row is anything
+    _check(_kvq_run(dev, stream, lambda handle: (_lib or load_library()).fa_kvcache_append_quant(
+        k.data_ptr(), v.data_ptr(), ks[0] if T > 1 else dense, vs[0] if T > 1 else dense, kpages.data_ptr(),
+        vpages.data_ptr(), cu_seqlens_new.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), B, Hkv, T,
+        int(max_seqlen_new), num_pages, page_size, max_blocks, d, bits, handle)), "fa_kvcache_append_quant")
 
 
 def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, max_seqlen, H, d, bits,
@@ -486,20 +504,17 @@ def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, 
     """The last cu_seqlens[b+1] - cu_seqlens[b] rows of each sequence as k, v [total, H, d] (out_dtype), KV head
     h / (H / Hkv) for head h: what forward_varlen takes."""
     dev = _kvq_device(kpages, "kpages")
-    page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
-    _kvq_check(dev, (cu_seqlens, "cu_seqlens", torch.int32))
-    if cu_seqlens.shape != (B + 1,):
-        raise ValueError("cu_seqlens must be [B + 1]")
+    num_pages, Hkv, page_size, B, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits, cu_seqlens)
     total = int(total)
 
     def call(handle):
         k = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
         v = torch.empty_like(k)
         if total:
-            _check(load_library().fa_kvcache_read_quant(
+            _check((_lib or load_library()).fa_kvcache_read_quant(
                 kpages.data_ptr(), vpages.data_ptr(), cu_seqlens.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
-                k.data_ptr(), v.data_ptr(), B, H, kpages.shape[1], total, int(max_seqlen), kpages.shape[0], page_size,
-                max_blocks, d, bits, _DT[out_dtype], handle), "fa_kvcache_read_quant")
+                k.data_ptr(), v.data_ptr(), B, H, Hkv, total, int(max_seqlen), num_pages, page_size, max_blocks, d, bits,
+                _DT[out_dtype], handle), "fa_kvcache_read_quant")
         return k, v
 
     return _kvq_run(dev, stream, call)
@@ -510,26 +525,24 @@ def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None
     """decode_paged over a quantised cache: o [B,H,d] and lse [B,H] for q [B,H,d] (bf16), pools
     [num_pages,Hkv,page bytes] (uint8), block_table int32 [B,max_blocks] and kv_lens int32 [B] (device)."""
     dev = _kvq_device(q, "q")
-    _kvq_check(dev, (q, "q", torch.bfloat16))
-    if q.dim() != 3:
-        raise ValueError("q must be [B, H, d]")
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bfloat16 tensor [B, H, d]")
     B, H, d = q.shape
-    page_size, rows, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
+    num_pages, Hkv, page_size, rows, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
     if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
     if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != dev):
         raise ValueError("ws must be a tensor on device %d" % dev)
-    Hkv = kpages.shape[1]
 
     def call(handle):
         w = ws
         if w is None:
             w = workspace(_kvq_sizes(B, H, Hkv, max_blocks, page_size, d, bits), q.device)
-        o = torch.empty((B, H, d), dtype=out_dtype, device=q.device)
+        o = torch.empty_like(q, dtype=out_dtype)
         lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        _check(load_library().fa_decode_paged_quant(
+        _check((_lib or load_library()).fa_decode_paged_quant(
             q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
-            lse.data_ptr(), B, H, Hkv, kpages.shape[0], page_size, max_blocks, d, bits,
+            lse.data_ptr(), B, H, Hkv, num_pages, page_size, max_blocks, d, bits,
             1.0 / math.sqrt(d) if scale is None else scale, _DT[out_dtype], w.data_ptr(), w.numel() * w.element_size(),
             handle), "fa_decode_paged_quant")
         return o, lse
