@@ -508,7 +508,7 @@ def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, 
     total = int(total)
 
     def call(handle):
-        k = torch.empty((total, H, d), dtype=out_dtype, device=kpages.device)
+        k = kpages.new_empty((total, H, d), dtype=out_dtype)
         v = torch.empty_like(k)
         if total:
             _check((_lib or load_library()).fa_kvcache_read_quant(
@@ -537,9 +537,9 @@ def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None
     def call(handle):
         w = ws
         if w is None:
-            w = workspace(_kvq_sizes(B, H, Hkv, max_blocks, page_size, d, bits), q.device)
+            w = kpages.new_empty(_kvq_sizes(B, H, Hkv, max_blocks, page_size, d, bits))
         o = torch.empty_like(q, dtype=out_dtype)
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H), dtype=torch.float32)
         _check((_lib or load_library()).fa_decode_paged_quant(
             q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
             lse.data_ptr(), B, H, Hkv, num_pages, page_size, max_blocks, d, bits,

@@ -263,7 +263,7 @@ def check_decode(dev, q, kpool, vpool, table, lens, bits, scale, dtypes=(torch.f
         inf = np.isneginf(lse_ref)
         assert np.array_equal(np.isneginf(lse), inf)
         fin = ~inf & ~np.isnan(lse_ref)
-        assert (np.abs(lse - lse_ref)[fin] <= tol_l[fin]).all()
+        assert (np.abs(lse[fin] - lse_ref[fin]) <= tol_l[fin]).all()
     return o_ref, lse_ref
 
 
@@ -480,3 +480,138 @@ def test_decode_streams_and_repeats(cuda_device):
     torch.cuda.synchronize()
     assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in got)
     assert fa.fa_check_status() == fa.FA_OK
+
+
+def test_decode_graphs_that_share_a_workspace(cuda_device):
+    """Two captured graphs of different shapes with one workspace, replayed in turn with eager calls between them: each
+    gives what its call alone gave, bit for bit, whatever the workspace held."""
+    dev, bits, d, Hkv = cuda_device, 4, 128, 2
+    calls = []
+    for seed, (lens, H, ps) in enumerate((([2500, 40, 0], 8, 64), ([17, 900], 4, 16))):
+        table, pages = make_table(lens, ps, 1, seed=seed)
+        kd, vd = (torch.from_numpy(ref.random_pool(pages, Hkv, ps, d, bits, seed=100 + 2 * seed + i)).to(dev) for i in (0, 1))
+        q = torch.randn(len(lens), H, d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).to(dev)
+        calls.append((q, kd, vd, i32(table, dev), i32(lens, dev), bits))
+    ws = fa.workspace(max(fa.fa_decode_paged_quant_workspace_size(c[0].shape[0], c[0].shape[1], Hkv, c[3].shape[1],
+                                                                  c[1].shape[2] // ref.row_bytes(d, bits), d, bits)
+                          for c in calls), dev)
+    alone = [fa.decode_paged_quant(*c) for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fa.decode_paged_quant(*c, ws=ws))
+        graphs.append(g)
+    for i in range(6):
+        ws.random_(0, 256)
+        for x in outs[i % 2]:
+            x.fill_(7.0)
+        graphs[i % 2].replay()
+        fa.decode_paged_quant(*calls[(i + 1) % 2], ws=ws)
+        assert all(torch.equal(a, b) for a, b in zip(outs[i % 2], alone[i % 2]))
+    assert fa.fa_check_status() == fa.FA_OK
+
+
+def attention64(q, kp, vp, table, lens, bits, scale, d):
+    """(o, lse, greatest |v| and greatest sum of the terms' magnitudes) in 64 bits on the GPU over what the cache reads back as."""
+    B, H = q.shape[:2]
+    cu = torch.cat([torch.zeros_like(lens[:1]), lens.cumsum(0).to(torch.int32)])
+    n = lens.tolist()
+    k, v = fa.kvcache_read_quant(kp, vp, cu, table, lens, sum(n), max(n), H, d, bits, out_dtype=torch.float32)
+    o = torch.zeros(B, H, d, dtype=torch.float64, device=q.device)
+    lse = torch.full((B, H), -math.inf, dtype=torch.float64, device=q.device)
+    X = 0.0
+    for b in range(B):
+        if n[b] == 0:
+            continue
+        kb, vb = (x[int(cu[b]):int(cu[b + 1])].double() for x in (k, v))
+        x = torch.einsum("hd,nhd->hn", q[b].double(), kb) * scale
+        # |lo| + s c is at most |value| + 2 |lo|, and |lo| below 4 in these pools
+        X = max(X, float((torch.einsum("hd,nhd->hn", q[b].double().abs(), kb.abs() + 8.0) * scale).max()))
+        lse[b] = torch.logsumexp(x, 1)
+        o[b] = torch.einsum("hn,nhd->hd", torch.softmax(x, 1), vb)
+    return o, lse, float(v.abs().max()), X
+
+
+@pytest.mark.parametrize("lens,H,Hkv,ps,d,bits", [
+    ([400000], 4, 1, 1024, 64, 4),                    # one long context over all CTAs
+    ([90000, 3], 2, 2, 65536, 128, 8),                # the largest pages
+    ([i % 7 * (i % 3) for i in range(3000)], 2, 1, 16, 64, 4),  # thousands of tiny sequences, most CTAs with many
+    ([70, 0, 1] * 50, 6, 3, 32, 256, 4),
+])
+def test_decode_sizes(cuda_device, lens, H, Hkv, ps, d, bits):
+    """Sizes that a plain loop cannot check: attention in 64 bits over the values that the cache reads back as (fp32,
+    2^-24 off).  The tolerances are those of kvq_reference.decode with every |v|, |v - o| and s c at twice the
+    greatest |v|, and 2^-23 of each score step for the read-back's rounding; a warp's sums have up to 400000 / 16 / 1776
+    steps here, 2^-23 * 17 each on the low nibbles."""
+    dev = cuda_device
+    table, pages = make_table(lens, ps, 1, seed=9)
+    kd, vd = (torch.from_numpy(ref.random_pool(pages, Hkv, ps, d, bits, seed=110 + i)).to(dev) for i in (0, 1))
+    q = torch.randn(len(lens), H, d, generator=torch.Generator().manual_seed(111)).to(torch.bfloat16).to(dev)
+    scale = 1.0 / math.sqrt(d)
+    table, lens_t = i32(table, dev), i32(lens, dev)
+    o_ref, lse_ref, top, X = attention64(q, kd, vd, table, lens_t, bits, scale, d)
+    o, lse = fa.decode_paged_quant(q, kd, vd, table, lens_t, bits)
+    assert fa.fa_check_status() == fa.FA_OK
+    ex = 2.0 ** -19 * X + 2.0 ** -21
+    steps = max(2, max(lens) // 16 // 1776 + 1)
+    assert float((o - o_ref).abs().max()) <= 2 * top * (2.0 ** -10 + 2 * ex + steps * 17 * 2.0 ** -23 + max(lens) * 2.0 ** -31 * 31)
+    fin = ~torch.isneginf(lse_ref)
+    assert torch.equal(torch.isneginf(lse), ~fin)
+    assert float((lse - lse_ref)[fin].abs().max()) <= ex + 2.0 ** -22 * float(lse_ref[fin].abs().max())
+    zero = lens_t == 0
+    assert (o[zero] == 0).all()
+
+
+def test_nothing_is_written_after_a_timeout(cuda_device):
+    """Once a wait anywhere in the library has run out (the fault-injection build), the calls write nothing until
+    fa_check_status has returned that."""
+    import ctypes
+
+    from exact_io_aware_94_b200 import build as fa_build
+
+    lib = ctypes.CDLL(fa_build.build(test_hooks=True))
+    vp, i, f, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
+    lib.fa_test_inject_fault.argtypes = [i]
+    lib.fa_forward.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp]
+    lib.fa_kvcache_append_quant.argtypes = [vp, vp, ll, ll, vp, vp, vp, vp, vp] + [i] * 9 + [vp]
+    lib.fa_kvcache_read_quant.argtypes = [vp] * 7 + [i] * 11 + [vp]
+    lib.fa_decode_paged_quant.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp, sz, vp]
+    lib.fa_check_status.argtypes = [vp]
+    dev, d, bits, H, Hkv, ps, n = cuda_device, 128, 4, 4, 2, 16, 40
+    st = torch.cuda.current_stream().cuda_stream
+    x = torch.randn(256, H, d, generator=torch.Generator().manual_seed(120)).to(torch.bfloat16).to(dev)
+    out, lse = torch.zeros(1, 1, 256, d, device=dev), torch.zeros(1, 1, 256, device=dev)
+    kd, vd = (torch.from_numpy(ref.random_pool(3, Hkv, ps, d, bits, seed=s)).to(dev) for s in (121, 122))
+    pools = [kd.clone(), vd.clone()]
+    table, lens, cu = i32([[2, 0, 1]], dev), i32([n], dev), i32([0, n], dev)
+    o, l, ko, vo = (torch.full(s, 7.0, device=dev) for s in ((1, H, d), (1, H), (n, H, d), (n, H, d)))
+    ws = fa.workspace(fa.fa_decode_paged_quant_workspace_size(1, H, Hkv, 3, ps, d, bits), dev)
+
+    def calls():
+        k = x[:n, :Hkv].contiguous()
+        assert lib.fa_kvcache_append_quant(k.data_ptr(), k.data_ptr(), Hkv * d, Hkv * d, kd.data_ptr(), vd.data_ptr(),
+                                           cu.data_ptr(), table.data_ptr(), lens.data_ptr(), 1, Hkv, n, n, 3, ps, 3, d,
+                                           bits, st) == fa.FA_OK
+        assert lib.fa_kvcache_read_quant(kd.data_ptr(), vd.data_ptr(), cu.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                         ko.data_ptr(), vo.data_ptr(), 1, H, Hkv, n, n, 3, ps, 3, d, bits, fa.FA_DT_F32,
+                                         st) == fa.FA_OK
+        assert lib.fa_decode_paged_quant(x.data_ptr(), kd.data_ptr(), vd.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                                         o.data_ptr(), l.data_ptr(), 1, H, Hkv, 3, ps, 3, d, bits, 0.1, fa.FA_DT_F32,
+                                         ws.data_ptr(), ws.numel(), st) == fa.FA_OK
+        torch.cuda.synchronize()
+
+    assert lib.fa_check_status(None) == fa.FA_OK
+    assert lib.fa_test_inject_fault(1) == fa.FA_OK  # a K tile of the next forward is never loaded
+    q = x[:, 0].contiguous()
+    assert lib.fa_forward(q.data_ptr(), q.data_ptr(), q.data_ptr(), out.data_ptr(), lse.data_ptr(), 1, 1, 256, 256, d, 0.1,
+                          0, fa.FA_DT_F32, st) == fa.FA_OK
+    torch.cuda.synchronize()
+    calls()
+    assert torch.equal(kd, pools[0]) and torch.equal(vd, pools[1])
+    assert all((t == 7.0).all() for t in (o, l, ko, vo))
+    assert lib.fa_check_status(None) == fa.FA_ERR_TIMEOUT
+    calls()
+    assert lib.fa_check_status(None) == fa.FA_OK
+    assert not torch.equal(kd, pools[0]) and all(torch.isfinite(t).all() and not (t == 7.0).any() for t in (o, l, ko, vo))
