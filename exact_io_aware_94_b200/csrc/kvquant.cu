@@ -335,35 +335,43 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p) {
     const float inv_row = 1.0f / static_cast<float>(row);
     const uint32_t block_bytes = static_cast<uint32_t>(F::kRowBytes) << p.page_shift;
     const bool wide = p.wide;
-    for (int e0 = 0; e0 < total; e0 += kKvqThreads) {
-        const int e = e0 + threadIdx.x;
-        const int at = min(e, total - C + piece.c);  // the last head's, for threads past the end
-        const int i = kvq_div(at, inv_row), h = static_cast<unsigned>(at - i * row) / C;
-        const int r = static_cast<unsigned>(pos0 + i) % kKvqTile;
-        const size_t off = s_tile[i] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * block_bytes;
-        const uint8_t* kt = p.kpages + off;
-        const uint8_t* vt = p.vpages + off;
-        const uint8_t* kd = kt + piece.k_off + r * F::kPlaneBytes;
-        const uint8_t* vd = vt + piece.v_off + r * F::kPlaneBytes;
-        uint32_t kc[BITS / 2], vc[BITS / 2], x[BITS / 2];
-        if constexpr (BITS == 4) {
-            kc[0] = *reinterpret_cast<const uint32_t*>(kd);
-            kc[1] = *reinterpret_cast<const uint32_t*>(kd + piece.kUnitStepK);
-            x[0] = *reinterpret_cast<const uint32_t*>(vd);
-            x[1] = *reinterpret_cast<const uint32_t*>(vd + piece.kUnitStepV);
-        } else {
-            const uint2 k0 = *reinterpret_cast<const uint2*>(kd), k1 = *reinterpret_cast<const uint2*>(kd + piece.kUnitStepK);
-            const uint2 v0 = *reinterpret_cast<const uint2*>(vd), v1 = *reinterpret_cast<const uint2*>(vd + piece.kUnitStepV);
-            kc[0] = k0.x, kc[1] = k0.y, kc[2] = k1.x, kc[3] = k1.y;
-            x[0] = v0.x, x[1] = v0.y, x[2] = v1.x, x[3] = v1.y;
+    constexpr int kAtOnce = 2;  // pieces whose loads are in flight together
+    for (int e0 = 0; e0 < total; e0 += kAtOnce * kKvqThreads) {
+        uint32_t kc[kAtOnce][BITS / 2], vx[kAtOnce][BITS / 2], kp[kAtOnce], vp[kAtOnce];
+        size_t to[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int e = min(e0 + j * kKvqThreads + static_cast<int>(threadIdx.x), total - C + piece.c);  // the last head's past the end
+            const int i = kvq_div(e, inv_row), h = static_cast<unsigned>(e - i * row) / C;
+            const int r = static_cast<unsigned>(pos0 + i) % kKvqTile;
+            const size_t off = s_tile[i] + static_cast<uint64_t>(static_cast<uint32_t>(h)) * block_bytes;
+            const uint8_t* kt = p.kpages + off;
+            const uint8_t* vt = p.vpages + off;
+            const uint8_t* kd = kt + piece.k_off + r * F::kPlaneBytes;
+            const uint8_t* vd = vt + piece.v_off + r * F::kPlaneBytes;
+            if constexpr (BITS == 4) {
+                kc[j][0] = *reinterpret_cast<const uint32_t*>(kd);
+                kc[j][1] = *reinterpret_cast<const uint32_t*>(kd + piece.kUnitStepK);
+                vx[j][0] = *reinterpret_cast<const uint32_t*>(vd);
+                vx[j][1] = *reinterpret_cast<const uint32_t*>(vd + piece.kUnitStepV);
+            } else {
+                const uint2 k0 = *reinterpret_cast<const uint2*>(kd), k1 = *reinterpret_cast<const uint2*>(kd + piece.kUnitStepK);
+                const uint2 v0 = *reinterpret_cast<const uint2*>(vd), v1 = *reinterpret_cast<const uint2*>(vd + piece.kUnitStepV);
+                kc[j][0] = k0.x, kc[j][1] = k0.y, kc[j][2] = k1.x, kc[j][3] = k1.y;
+                vx[j][0] = v0.x, vx[j][1] = v0.y, vx[j][2] = v1.x, vx[j][3] = v1.y;
+            }
+            kp[j] = *reinterpret_cast<const uint32_t*>(kt + piece.p_off + r * F::kParamBytes);
+            vp[j] = *reinterpret_cast<const uint32_t*>(vt + piece.p_off + r * F::kParamBytes);
+            to[j] = (static_cast<size_t>(first + i) * p.H + h * G) * D + piece.c * 16;
         }
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(kt + piece.p_off + r * F::kParamBytes);
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(vt + piece.p_off + r * F::kParamBytes);
-        piece.from_stored(x, vc);
-        if (e >= total) continue;
-        const size_t to = (static_cast<size_t>(first + i) * p.H + h * G) * D + piece.c * 16;
-        kvq_emit<D, BITS, F32>(kc, kp, p.k_out, to, G, wide);
-        kvq_emit<D, BITS, F32>(vc, vp, p.v_out, to, G, wide);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            uint32_t vc[BITS / 2];
+            piece.from_stored(vx[j], vc);
+            if (e0 + j * kKvqThreads + static_cast<int>(threadIdx.x) >= total) continue;
+            kvq_emit<D, BITS, F32>(kc[j], kp[j], p.k_out, to[j], G, wide);
+            kvq_emit<D, BITS, F32>(vc, vp[j], p.v_out, to[j], G, wide);
+        }
     }
 }
 
