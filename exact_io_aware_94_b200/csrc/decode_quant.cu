@@ -16,12 +16,18 @@
 // it exactly down to 2^-29 of that, and to 2^-40 in absolute terms.
 //
 // Weights.  u = 2^6 2^(x - m), below 2^14 because the reference m follows the maximum to
-// within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head.  lo
-// and s are scaled by 2^-E, which keeps those of every unit below 2, so fp16 holds
-// their 8 bits down to 2^-17 of that; u s is rounded to fp16 again, u lo is not.  One
-// product of the rounded u with [lo of each group; ones] gives the sums of u lo and of u: the output is
-// divided by the sum of the same rounded weights, so their errors only weigh values
-// against each other and a constant comes out exact.  lse takes the fp32 sum.
+// within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head, and
+// u s again.  s and the offsets are scaled by 2^-E, which keeps those of every unit below 2.
+// One product of the rounded u with [offset of each group; ones] gives the sums of u times the offset
+// and of u: the output is divided by the sum of the same rounded weights, so their errors only weigh values against
+// each other.  lse takes the fp32 sum.
+//
+// Long sums.  The matrix instruction truncates its fp32 accumulator, half a unit in the last place
+// a step on average, and sums of p s c and of p lo over many keys are large and of
+// opposite sign: over 10,000 keys a warp that bias was 2 % of the output.  So half of the keys of
+// every product (t + 8 and t + 12) enter as lo + C s - s (C - c), C = 2^BITS - 1: the complement
+// of the code, which the AND takes with no instruction more, a negative s and the offset lo + C s.
+// The two halves' terms cancel as they are summed, and the accumulators stay as small as the result.
 //
 // mma.sync m16n8k16 with the keys (scores) or dimensions (output) as the 16 rows and
 // the heads that share the KV head as the 8 columns: NT = 1 or 2 tiles of 8.  Scores
@@ -102,7 +108,7 @@ struct Cfg {
     static constexpr int kStageBytes = 2 * kHalf;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
-    // V's s and lo of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], lo [tile][group][key % 4][key / 4]
+    // V's s and offsets of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], offset [tile][group][key % 4][key / 4]
     static constexpr int kSBytes = kBlocks * F::kGroups * 32;
     static constexpr int kPairs = kBlocks * F::kGroups / 4;  // pairs of keys of a group that a thread converts
     static_assert(kPairs > 0, "a unit has a pair for every thread");
@@ -376,6 +382,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     const int pair_group = lane % NG;
     auto pair_of = [&](int i) { return i * (32 / NG) + lane / NG; };
     auto pair_key = [&](int i) { return (pair_of(i) / 2) % 4 + 8 * (pair_of(i) % 2); };
+    // keys t + 8 and t + 12 enter by their complements (32 / NG and so a thread's pairs are even steps apart)
+    const bool complement = (lane / NG) % 2;
+    const float to_offset = complement ? static_cast<float>((1 << BITS) - 1) : 0.0f;  // offset = lo + this s
     float* sc = reinterpret_cast<float*>(smem + C::kScoreOff + warp * C::kScoreBytes);  // [head][key]: scores
     uint8_t* par = smem + C::kParOff + warp * C::kParBytes;
     auto first_part = [&](int w) { return reinterpret_cast<float*>(smem + C::kFirstOff) + w * HP * D; };
@@ -388,10 +397,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         const size_t head0 = static_cast<size_t>(cur.b) * p.H + cur.hkv * group + h_in;
 
         float o[NT][D / 16][4];
-        float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u lo of group r, sums of u
+        float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u times the offset of group r, sums of u
         float m[NT], l[NT];
         int E = -100;
-        float down = 0.0f;  // 2^-E
+        float down = 0.0f, s_down = 0.0f;  // 2^-E, and that with the sign of s in this thread's pairs
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
         uint32_t qz[NT][C::kZSteps][2];  // sums of q over a group, as the B operand of the lo product
@@ -562,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     const uint8_t* from = vs + kb * F::kTileBytes + F::kParamOff + j * F::kParamBytes + pair_group * 4;
                     const uint32_t x = *reinterpret_cast<const uint32_t*>(from);
                     const uint32_t y = *reinterpret_cast<const uint32_t*>(from + 4 * F::kParamBytes);
-                    const uint32_t sp = pack_f16x2(s_of(x) * down, s_of(y) * down), zp = pack_f16x2(lo_of(x) * down, lo_of(y) * down);
+                    const uint32_t sp = pack_f16x2(s_of(x) * s_down, s_of(y) * s_down);
+                    const uint32_t zp = pack_f16x2(fmaf(s_of(x), to_offset, lo_of(x)) * down, fmaf(s_of(y), to_offset, lo_of(y)) * down);
                     over |= sp | zp;
                     *reinterpret_cast<uint32_t*>(par + ((kb * 4 + j % 4) * NG + pair_group) * 8 + j / 8 * 4) = sp;
                     *reinterpret_cast<uint32_t*>(par + C::kSBytes + (kb * NG + pair_group) * 32 + (j % 4) * 8 + j / 8 * 4) = zp;
@@ -600,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t w = *reinterpret_cast<const uint32_t*>(
                             vs + (pair_of(i) / 8) * F::kTileBytes + F::kParamOff + (pair_key(i) + 4 * x) * F::kParamBytes + pair_group * 4);
-                        const uint32_t hi = w & 0x7FFF0000u, lo = (w << 16) & 0x7FFF0000u;
+                        const uint32_t hi = w & 0x7FFF0000u;
+                        const uint32_t lo = __float_as_uint(fmaf(s_of(w), to_offset, lo_of(w))) & 0x7FFFFFFFu;
                         top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
                     }
                 top = __reduce_max_sync(0xffffffffu, top);
@@ -627,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 }
                 E = e_new;
                 down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
+                s_down = complement ? -down : down;
                 __syncwarp();  // the scores have been read: not before the parameters are written anew
                 convert();
             }
@@ -689,13 +701,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                                 const uint32_t x = __byte_perm(c[0][w], c[1][w], sel);
                                 const uint32_t y = __byte_perm(c[2][w], c[3][w], sel);
                                 a0 = st ? __byte_perm(x, 0, 0x4341) : x & 0x00FF00FFu, a1 = a0 & 0x00F000F0u;
-                                a2 = st ? __byte_perm(y, 0, 0x4341) : y & 0x00FF00FFu, a3 = a2 & 0x00F000F0u;
+                                a2 = (st ? ~(y >> 8) : ~y) & 0x00FF00FFu, a3 = a2 & 0x00F000F0u;
                             } else {
                                 const int sel = st ? 0x7632 : 0x5410;
                                 const uint32_t x = __byte_perm(c[0][w], c[1][w], sel);
                                 const uint32_t y = __byte_perm(c[2][w], c[3][w], sel);
                                 a0 = x & 0x00FF00FFu, a1 = (x >> 8) & 0x00FF00FFu;
-                                a2 = y & 0x00FF00FFu, a3 = (y >> 8) & 0x00FF00FFu;
+                                a2 = ~y & 0x00FF00FFu, a3 = ~(y >> 8) & 0x00FF00FFu;
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)

@@ -119,12 +119,13 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
     nats) and at most 14 fp32 roundings on the way (two accumulations a group that may truncate, d / 32 + 2 fused
     sums), it is off by less than 2^-20 X, and the exponential by 2^-22 more.  lse adds its own fp32 rounding.
     A probability's weight u is rounded to fp16 for the output, which is divided by the sum of the rounded weights:
-    with u (1 + e), |e| <= 2^-11, the output moves by sum(p e (v - o)) at first order.  The product u s that weighs
-    a code is rounded to fp16 again: 2^-11 of sum(p s c).  fp16 steps end at 2^-24: as the greatest u is at least
-    2^6 and lo and s are scaled by the power of two above the greatest, M, each of n keys adds at most
-    2^-25 / 2^6 (|v - o| + 2 M c), and the rounding of s or lo itself 2^-25 * 2 M (c + 1) on average over the keys.
-    A code's low nibbles are summed as the difference of two sums up to 16 times as large: at most 16 steps a warp
-    at these tests' sizes, which may truncate (2^-23), 2^-14 of sum(p s c) in all.
+    with u (1 + e), |e| <= 2^-11, the output moves by sum(p e (v - o)) at first order.  Half of the keys enter as
+    hi - s (C - c), hi = lo + C s rounded to fp16 and C the greatest code; the product of u and s that weighs c or
+    C - c is rounded to fp16 too: 2^-11 of sum(p (|hi| + s C)), which covers either.  fp16 steps end at 2^-24: as the
+    greatest u is at least 2^6 and lo, hi and s are scaled by the power of two above the greatest, M, each of n keys
+    adds at most 2^-25 / 2^6 (|v - o| + 2 M C), and the rounding of s, lo or hi itself 2^-25 * 2 M (C + 1) on average
+    over the keys.  A code's low nibbles are summed as the difference of two sums up to 16 times as large: at most
+    16 steps a warp at these tests' sizes, which may truncate (2^-23), 2^-14 of sum(p s C) in all.
     The factor 1 + 2^-8 covers the products of these errors."""
     B, H, d = q.shape
     Hkv = kpool.shape[1]
@@ -149,10 +150,12 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
                 ex = 2.0 ** -20 * X.max() + 2.0 ** -21
                 v = (vlo + vs * vc)[:, g]
                 o[b, h] = p @ v
-                far, M = np.abs(v - o[b, h]), np.nanmax([np.nanmax(np.abs(vlo[:, g])), np.nanmax(vs[:, g])])
                 top = 2 ** bits - 1
+                vhi, spread = np.abs(vlo + top * vs)[:, g], (top * vs)[:, g]
+                far, M = np.abs(v - o[b, h]), max(np.nanmax(vhi), np.nanmax(np.abs(vlo[:, g])), np.nanmax(vs[:, g]))
                 tol_o[b, h] = (1 + 2.0 ** -8) * (
-                    2.0 ** -11 * (p @ far) + (2.0 ** -11 + 2.0 ** -14) * (p @ (vs * vc)[:, g]) + 2 * ex * (p @ (np.abs(vlo) + vs * vc)[:, g])
+                    2.0 ** -11 * (p @ far + p @ vhi) + (2.0 ** -11 + 2.0 ** -14) * (p @ spread)
+                    + 2 * ex * (p @ (np.abs(vlo) + vs * vc)[:, g])
                     + n * 2.0 ** -31 * (far.max(0) + 2 * M * top) + 2.0 ** -24 * M * (top + 1))
                 tol_l[b, h] = ex + 2.0 ** -22 * abs(lse[b, h])
     return o, lse, tol_o, tol_l
