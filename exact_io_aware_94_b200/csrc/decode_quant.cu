@@ -66,9 +66,11 @@ constexpr int NC = 4;               // warps of a CTA
 constexpr int kThreads = 32 * NC;
 // CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone
 // takes nt d / 4.  (One more with q in shared memory was no faster: 281 -> 289 us at d = 128, 48 -> 51 us at
-// d = 256.)
-__host__ __device__ constexpr int ctas_per_sm(int d, int nt) { return nt * d <= 64 ? 4 : nt * d <= 128 ? 3 : 2; }
-__host__ __device__ constexpr int max_ctas(int d, int nt) { return kMaxSms * ctas_per_sm(d, nt); }
+// d = 256.)  At d = 64 in 4 bits, three leave the shared memory for units of 64 keys.
+__host__ __device__ constexpr int ctas_per_sm(int d, int bits, int nt) {
+    return nt * d <= 64 && bits == 8 ? 4 : nt * d <= 128 ? 3 : 2;
+}
+__host__ __device__ constexpr int max_ctas(int d, int bits, int nt) { return kMaxSms * ctas_per_sm(d, bits, nt); }
 constexpr float kRefBits = 6.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 constexpr float kNoMax = -1e30f;    // the maximum of no score: finite, so that no difference is NaN
@@ -94,14 +96,15 @@ struct DecodeQuantParams {
 template <int D, int BITS, int NT>
 struct Cfg {
     using F = KvqFormat<D, BITS>;
-    static constexpr int kCtas = ctas_per_sm(D, NT);
+    static constexpr int kCtas = ctas_per_sm(D, BITS, NT);
     static constexpr int kBudget = 228 * 1024 / kCtas - 1024;    // of a CTA
     static constexpr int kFixed = NC * 8 * NT * D * 4 + 512;     // the warps' first parts
     // a warp's scores, parameters and stages of a unit of n tiles
     static constexpr int per_warp(int n, int stages) {
         return 8 * NT * (16 * n + 4) * 4 + n * F::kGroups * 64 + 8 * NT * 8 + 64 + stages * 2 * n * F::kTileBytes;
     }
-    static constexpr int kBlocks = kFixed + NC * per_warp(2, 2) <= kBudget ? 2 : 1;  // tiles of a unit
+    // tiles of a unit: what is done once a unit is the smaller a part, the more it has
+    static constexpr int kBlocks = D == 64 && kFixed + NC * per_warp(4, 2) <= kBudget ? 4 : kFixed + NC * per_warp(2, 2) <= kBudget ? 2 : 1;
     static constexpr int S = kFixed + NC * per_warp(kBlocks, 4) <= kBudget ? 4 : kFixed + NC * per_warp(kBlocks, 3) <= kBudget ? 3 : 2;
     static constexpr int KT = 16 * kBlocks;
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     const int w0 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * warp / NC);
     const int w1 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * (warp + 1) / NC);
     int v_load = w0, s_load = 0;
-    int key = 0, left = 0, page0 = 0, page1 = 0;  // of unit v_load
+    int key = 0, left = 0, page0 = 0, page1 = 0;  // of unit v_load (four tiles: page0 of lane i is tile i's)
     int set_end = 0;                               // of ahead
     const int* table = nullptr;
     size_t head_off = 0;
@@ -336,9 +339,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         }
         key = (v_load - ahead.begin) * KT;
         left = ahead.len - key;
-        const int* entry = table + (key >> p.page_shift);
-        page0 = entry[0];
-        if (two && left > 16) page1 = entry[1];
+        if constexpr (NB == 4) {
+            if (lane < NB && lane * 16 < left) page0 = table[(key + lane * 16) >> p.page_shift];
+        } else {
+            const int* entry = table + (key >> p.page_shift);
+            page0 = entry[0];
+            if (two && left > 16) page1 = entry[1];
+        }
     };
     auto page_in = [&](int page) {
         if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
@@ -347,6 +354,24 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     };
     auto issue = [&]() {
         if (v_load < w1) {
+            const uint32_t dst = ring_lane + s_load * C::kStageBytes;
+            if constexpr (NB == 4) {
+                const int page = lane < NB && lane * 16 < left ? page_in(page0) : 0;
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb) {
+                    const uint32_t pg = __shfl_sync(0xffffffffu, page, kb);
+                    if (kb * 16 >= left) continue;
+                    const size_t off = static_cast<uint64_t>(pg) * page_stride16 * 16 + head_off +
+                                       static_cast<uint32_t>(((key + kb * 16) & ((1 << p.page_shift) - 1)) / kKvqTile) * F::kTileBytes;
+#pragma unroll
+                    for (int i = 0; i < F::kTileBytes; i += 512) {
+                        if (i + 512 <= F::kTileBytes || i + lane * 16 < F::kTileBytes) {
+                            copy16(dst + kb * F::kTileBytes + i, p.kpages + off + i);
+                            copy16(dst + C::kHalf + kb * F::kTileBytes + i, p.vpages + off + i);
+                        }
+                    }
+                }
+            } else {
             const uint32_t tile = (key & ((1 << p.page_shift) - 1)) / kKvqTile;
             const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page0))) * page_stride16 * 16 + head_off +
                                tile * F::kTileBytes;
@@ -354,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             size_t off1 = off;
             if (two && left > 16)
                 off1 = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page1))) * page_stride16 * 16 + head_off - F::kTileBytes;
-            const uint32_t dst = ring_lane + s_load * C::kStageBytes;
             const int bytes = left > 16 ? C::kHalf : F::kTileBytes;
 #pragma unroll
             for (int i = 0; i < C::kHalf; i += 512) {
@@ -363,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     copy16(dst + i, p.kpages + at + i);
                     copy16(dst + C::kHalf + i, p.vpages + at + i);
                 }
+            }
             }
             ++v_load;
             s_load = s_load + 1 == S ? 0 : s_load + 1;
@@ -843,10 +868,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 // CTAs has P - 1 such blocks, each of which merges a share of its outputs, four at a time.  What bounds it
 // is the latency of its loads, so all that a thread needs is asked for at once: 6 us with the loads in turn, 2 us so.
 constexpr int kCombineThreads = 256;
-template <int D, int NT>
+template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
     constexpr int HP = 8 * NT, D4 = D / 4;
-    __shared__ float s_w[HP][max_ctas(D, NT)];  // of part c0 + i, normalised
+    __shared__ float s_w[HP][max_ctas(D, BITS, NT)];  // of part c0 + i, normalised
     __shared__ float4 s_o[kCombineThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x + 1;
@@ -979,7 +1004,7 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_decode_quant_combine<D, NT>, p);
+    return cudaLaunchKernelEx(&cfg, fa_decode_quant_combine<D, BITS, NT>, p);
 }
 
 // 8-head tiles of a set: two (O takes NT D / 4 registers a thread) only where a second
@@ -990,9 +1015,9 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct Workspace {
     size_t lse, cut, used, total;  // offsets of the arrays after part_o
 };
-Workspace workspace_of(int H, int Hkv, int d) {
+Workspace workspace_of(int H, int Hkv, int d, int bits) {
     const int nt = tiles_of(H / Hkv, d);
-    const size_t ctas = max_ctas(d, nt), heads = 8 * nt;
+    const size_t ctas = max_ctas(d, bits, nt), heads = 8 * nt;
     Workspace w{};
     w.lse = up256(2 * ctas * heads * d * sizeof(float));
     w.cut = w.lse + up256(2 * ctas * heads * sizeof(float));
@@ -1009,7 +1034,7 @@ using namespace fa;
 
 extern "C" size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits) {
     if (kvq_check_pool(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
-    return workspace_of(H, Hkv, d).total;
+    return workspace_of(H, Hkv, d, bits).total;
 }
 
 extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
@@ -1030,7 +1055,7 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.cap = max_blocks * page_size;
     // units are counted in int32, a little past the last one too; 16 keys is the shortest
     if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
-    const Workspace at = workspace_of(H, Hkv, d);
+    const Workspace at = workspace_of(H, Hkv, d, bits);
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < at.total) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;
