@@ -36,7 +36,9 @@
 // A fragments are one 16-byte (K) or 8-byte (V) shared-memory load a key and plane,
 // which is what the cache's order of dimensions inside a token is for.
 //
-// Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  The units
+// Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  To begin and end
+// a set costs a warp about as much as 96 keys, so a set counts as that many units more,
+// ahead of its own (batches with short sequences: 5 % of the time).  The units
 // of the whole batch, in that order, are cut into equal runs, one a CTA, and a CTA's run
 // into equal runs for its four warps.  A warp copies its units into a ring of S
 // stages of its own with 16-byte asynchronous copies (a 16-token tile of K or of V is
@@ -86,7 +88,7 @@ struct DecodeQuantParams {
     int* status;
     float* part_o;    // [2 * CTAs][8 NT][D], normalised
     float* part_lse;  // [2 * CTAs][8 NT], base 2
-    int4* cut;        // [CTAs]: the set that is cut at a CTA's first unit: (first row of o, heads, first CTA of it, CTAs); or 0 CTAs
+    int4* cut;        // [CTAs]: the set that is cut at a CTA's first unit: (first row of o, heads, first CTA of it, CTAs); 0 CTAs if none is
     int* used;        // CTAs that have units
     int B, H, Hkv, num_pages, page_shift, max_blocks, cap, sets;  // sets: head sets of a KV head
     float scale, scale_log2;
@@ -107,6 +109,7 @@ struct Cfg {
     static constexpr int kBlocks = D == 64 && kFixed + NC * per_warp(4, 2) <= kBudget ? 4 : kFixed + NC * per_warp(2, 2) <= kBudget ? 2 : 1;
     static constexpr int S = kFixed + NC * per_warp(kBlocks, 4) <= kBudget ? 4 : kFixed + NC * per_warp(kBlocks, 3) <= kBudget ? 3 : 2;
     static constexpr int KT = 16 * kBlocks;
+    static constexpr int kVisit = (96 + KT - 1) / KT;      // units that a set counts for beside its own
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kHalf;
     static constexpr int HP = 8 * NT;  // heads of a set
@@ -196,16 +199,22 @@ template <int KT>
 __device__ __forceinline__ int units_of(int len) {
     return static_cast<int>((static_cast<unsigned>(len) + KT - 1) / KT);
 }
+// What a set of that length counts for.
+template <int KT, int kVisit>
+__device__ __forceinline__ int weight_of(int len) {
+    return len > 0 ? units_of<KT>(len) + kVisit : 0;
+}
 __device__ __forceinline__ int clamp_len(int len, int cap) { return min(max(len, 0), cap); }
 
 // floor(a / b) for 0 <= a < 2^42 and 0 < b < 2^31 with a quotient below 2^31 where b < 2^10, below 2^10 otherwise: the
 // quotient is at least 1 / b below the next integer, far more than its rounding to 53 bits.
 __device__ __forceinline__ int div_floor(long long a, int b) { return static_cast<int>(static_cast<double>(a) / static_cast<double>(b)); }
 
-// A place in the batch's order of units: the set that unit v belongs to.
-template <int KT>
+// A place in the batch's order of units: the set that place v belongs to.  Its own units
+// are the last n - kVisit of its places.
+template <int KT, int kVisit>
 struct Cursor {
-    int b, hkv, set, begin, n, len;  // sequence, KV head, head set, first unit, units, keys
+    int b, hkv, set, begin, n, len;  // sequence, KV head, head set, first place, places, keys
     __device__ __forceinline__ void seek(const DecodeQuantParams& p, int v) {
         while (v >= begin + n) {
             begin += n;
@@ -217,7 +226,7 @@ struct Cursor {
                 ++b;
                 len = clamp_len(p.kv_lens[b], p.cap);
             } while (len == 0);
-            n = units_of<KT>(len);
+            n = weight_of<KT, kVisit>(len);
         }
     }
 };
@@ -242,7 +251,7 @@ template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
     using C = Cfg<D, BITS, NT>;
     using F = KvqFormat<D, BITS>;
-    constexpr int KT = C::KT, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
+    constexpr int KT = C::KT, kVisit = C::kVisit, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may be set up while this one runs
@@ -259,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     for (int b = b0; b < b1; ++b) {
         const int len = p.kv_lens[b];
         if (blockIdx.x == 0 && (len < 0 || len > p.cap)) atomicCAS(p.status, 0, FA_ERR_KV_LEN);
-        mine += units_of<KT>(clamp_len(len, p.cap));
+        mine += weight_of<KT, kVisit>(clamp_len(len, p.cap));
     }
     int incl = mine;
 #pragma unroll
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         if (u0 >= lo && u0 < hi) {
             int at = lo;
             for (int b = b0; b < b1; ++b) {
-                const int len = clamp_len(p.kv_lens[b], p.cap), n = units_of<KT>(len);
+                const int len = clamp_len(p.kv_lens[b], p.cap), n = weight_of<KT, kVisit>(len);
                 if (u0 < at + n * HH) {
                     const int hh = (u0 - at) / n;
                     misc[1] = b, misc[2] = hh, misc[3] = at + hh * n, misc[4] = len;
@@ -312,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         }
     }
     __syncthreads();
-    Cursor<KT> cur{misc[1], misc[2] / p.sets, misc[2] % p.sets, misc[3], units_of<KT>(misc[4]), misc[4]};
+    Cursor<KT, kVisit> cur{misc[1], misc[2] / p.sets, misc[2] % p.sets, misc[3], weight_of<KT, kVisit>(misc[4]), misc[4]};
     const int group = p.H / p.Hkv;
 
     // ---- copies: this warp's units [w0, w1), unit w0 + i in stage i % S
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     const size_t block_bytes = static_cast<size_t>(F::kRowBytes) << p.page_shift;
     const uint32_t page_stride16 = static_cast<uint32_t>(block_bytes * p.Hkv / 16);
     const bool two = NB == 2 && p.page_shift == 4;  // the tiles of a unit lie in different pages
-    Cursor<KT> ahead = cur;
+    Cursor<KT, kVisit> ahead = cur;
     const int w0 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * warp / NC);
     const int w1 = u0 + static_cast<int>(static_cast<long long>(u1 - u0) * (warp + 1) / NC);
     int v_load = w0, s_load = 0;
@@ -336,8 +345,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             set_end = ahead.begin + ahead.n;
             table = p.block_table + static_cast<size_t>(ahead.b) * p.max_blocks;
             head_off = ahead.hkv * block_bytes + lane * 16;
+            v_load = max(v_load, ahead.begin + kVisit);
+            if (v_load >= w1) return;
         }
-        key = (v_load - ahead.begin) * KT;
+        key = (v_load - ahead.begin - kVisit) * KT;
         left = ahead.len - key;
         if constexpr (NB == 4) {
             if (lane < NB && lane * 16 < left) page0 = table[(key + lane * 16) >> p.page_shift];
@@ -416,7 +427,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     int s = 0;
     for (int at = w0; at < w1;) {
         cur.seek(p, at);
-        const int end = min(w1, cur.begin + cur.n);
+        const int end = min(w1, cur.begin + cur.n), own = cur.begin + kVisit;
+        if (end <= own) {  // no unit of the set itself is this warp's
+            at = end;
+            continue;
+        }
+        at = max(at, own);
         const int h_in = cur.set * HP;
         const int G = min(HP, group - h_in);  // heads of the set
         const size_t head0 = static_cast<size_t>(cur.b) * p.H + cur.hkv * group + h_in;
@@ -504,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             __syncwarp();
             uint8_t* ks = ring + s * C::kStageBytes;
             uint8_t* vs = ks + C::kHalf;
-            const int valid = v == last ? cur.len - (v - cur.begin) * KT : KT;
+            const int valid = v == last ? cur.len - (v - own) * KT : KT;
             if (valid < KT) {
                 // Slots past the last key may hold anything, tiles not copied too: their V parameters
                 // become zero (a zero probability would not cancel a NaN), their scores -inf below.
@@ -747,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
 
         // ---- the set's output, or this warp's part of it: thread (r, t) has dimensions 32 g + 4 r + [0, 4) of
         // heads 2 t, 2 t + 1
-        const bool before = at > cur.begin, after = end < cur.begin + cur.n;
+        const bool before = at > own, after = end < cur.begin + cur.n;
         const bool whole = !before && !after;
         float* part = before ? first_part(warp) : reinterpret_cast<float*>(ring);
         __syncwarp();  // the ring has been read
@@ -795,11 +811,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     }
 
     if (tid == 0) {
-        // for the combine kernel: the set of the CTA's first unit, if that is not the set's first one too
-        const int b = misc[1], hkv = misc[2] / p.sets, h_in = (misc[2] - hkv * p.sets) * HP, begin = misc[3];
-        const int c0 = div_floor((begin + 1LL) * n_cta - 1, U);
-        const int c1 = div_floor((begin + static_cast<long long>(units_of<KT>(misc[4]))) * n_cta - 1, U);
-        p.cut[cta] = make_int4(b * p.H + hkv * group + h_in, min(HP, group - h_in), c0, begin == u0 ? 0 : c1 - c0 + 1);
+        // for the combine kernel: the set of the CTA's first place, if earlier units of the set are another CTA's
+        const int b = misc[1], hkv = misc[2] / p.sets, h_in = (misc[2] - hkv * p.sets) * HP, own = misc[3] + kVisit;
+        const int c0 = div_floor((own + 1LL) * n_cta - 1, U);
+        const int c1 = div_floor((own + static_cast<long long>(units_of<KT>(misc[4]))) * n_cta - 1, U);
+        p.cut[cta] = make_int4(b * p.H + hkv * group + h_in, min(HP, group - h_in), c0, u0 > own ? c1 - c0 + 1 : 0);
     }
 
     // ---- the CTA's parts: those of one set are neighbours in the order first, last of warp 0, first, last of warp 1, ...
@@ -991,7 +1007,7 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1);
+    const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1 + C::kVisit);
     const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
     fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
@@ -1053,8 +1069,8 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     DecodeQuantParams p{};
     p.sets = (H / Hkv + 8 * nt - 1) / (8 * nt);
     p.cap = max_blocks * page_size;
-    // units are counted in int32, a little past the last one too; 16 keys is the shortest
-    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 1) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
+    // units are counted in int32, a little past the last one too; 16 keys is the shortest, with 6 more a set
+    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 7) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
     const Workspace at = workspace_of(H, Hkv, d, bits);
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < at.total) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
