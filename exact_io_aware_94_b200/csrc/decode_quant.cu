@@ -17,7 +17,8 @@
 //
 // Weights.  u = 2^6 2^(x - m), below 2^14 because the reference m follows the maximum to
 // within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head, and
-// u s again.  s and the offsets are scaled by 2^-E, which keeps those of every unit below 2.
+// u s again.  s and the offsets are scaled by 2^-E, which keeps those of every unit below 2; each group of dimensions has
+// an E of its own, so that one with large values takes nothing from the others.
 // One product of the rounded u with [offset of each group; ones] gives the sums of u times the offset
 // and of u: the output is divided by the sum of the same rounded weights, so their errors only weigh values against
 // each other.  lse takes the fp32 sum.
@@ -278,7 +279,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     }
     if (lane == 31) misc[8 + warp] = incl;
     __syncthreads();
-    if (misc[0]) return;
+    if (misc[0]) {  // the combine kernel may see the status cleared by then
+        if (tid == 0) {
+            p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+            if (blockIdx.x == 0) *p.used = 0;
+        }
+        return;
+    }
     int total = 0;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
@@ -383,22 +390,22 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     }
                 }
             } else {
-            const uint32_t tile = (key & ((1 << p.page_shift) - 1)) / kKvqTile;
-            const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page0))) * page_stride16 * 16 + head_off +
-                               tile * F::kTileBytes;
-            // where the unit's bytes lie: those before kTileBytes from off, the others from off1
-            size_t off1 = off;
-            if (two && left > 16)
-                off1 = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page1))) * page_stride16 * 16 + head_off - F::kTileBytes;
-            const int bytes = left > 16 ? C::kHalf : F::kTileBytes;
+                const uint32_t tile = (key & ((1 << p.page_shift) - 1)) / kKvqTile;
+                const size_t off = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page0))) * page_stride16 * 16 + head_off +
+                                   tile * F::kTileBytes;
+                // where the unit's bytes lie: those before kTileBytes from off, the others from off1
+                size_t off1 = off;
+                if (two && left > 16)
+                    off1 = static_cast<uint64_t>(static_cast<uint32_t>(page_in(page1))) * page_stride16 * 16 + head_off - F::kTileBytes;
+                const int bytes = left > 16 ? C::kHalf : F::kTileBytes;
 #pragma unroll
-            for (int i = 0; i < C::kHalf; i += 512) {
-                const size_t at = i + 512 <= F::kTileBytes ? off : i >= F::kTileBytes || i + lane * 16 >= F::kTileBytes ? off1 : off;
-                if ((i + 512 <= F::kTileBytes) || i + lane * 16 < bytes) {
-                    copy16(dst + i, p.kpages + at + i);
-                    copy16(dst + C::kHalf + i, p.vpages + at + i);
+                for (int i = 0; i < C::kHalf; i += 512) {
+                    const size_t at = i + 512 <= F::kTileBytes ? off : i >= F::kTileBytes || i + lane * 16 >= F::kTileBytes ? off1 : off;
+                    if ((i + 512 <= F::kTileBytes) || i + lane * 16 < bytes) {
+                        copy16(dst + i, p.kpages + at + i);
+                        copy16(dst + C::kHalf + i, p.vpages + at + i);
+                    }
                 }
-            }
             }
             ++v_load;
             s_load = s_load + 1 == S ? 0 : s_load + 1;
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         float o[NT][D / 16][4];
         float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u times the offset of group r, sums of u
         float m[NT], l[NT];
-        int E = -100;
+        int E = -100;                      // of group pair_group
         float down = 0.0f, s_down = 0.0f;  // 2^-E, and that with the sign of s in this thread's pairs
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
@@ -644,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                 grow |= mx[nt] > m[nt] + kGrowBits;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                uint32_t top = 0;  // greatest magnitude of the unit's parameters, as fp32 bits; NaN left out
+                uint32_t top = 0;  // greatest magnitude of the group's parameters in the unit, as fp32 bits; NaN left out
 #pragma unroll
                 for (int i = 0; i < C::kPairs; ++i)
 #pragma unroll
@@ -655,9 +662,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                         const uint32_t lo = __float_as_uint(fmaf(s_of(w), to_offset, lo_of(w))) & 0x7FFFFFFFu;
                         top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
                     }
-                top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+                for (int x = NG; x < 32; x *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
                 const int e_new = max(E, min(max(static_cast<int>(top >> 23) - 126, -100), 126));
-                const float fall = ex2_approx(static_cast<float>(E - e_new));
+                const float own_fall = ex2_approx(static_cast<float>(E - e_new));
+                float fall[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) fall[g] = __shfl_sync(0xffffffffu, own_fall, g);
+                const float fall_r = __shfl_sync(0xffffffffu, own_fall, r % NG);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float m_new = fmaxf(m[nt], mx[nt]);
@@ -665,16 +677,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
                     m[nt] = m_new;
                     l[nt] *= alpha;
                     const float al0 = __shfl_sync(0xffffffffu, alpha, 8 * t), al1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
-                    oc[nt][0] *= al0 * fall;
-                    oc[nt][1] *= al1 * fall;
+                    oc[nt][0] *= al0 * fall_r;
+                    oc[nt][1] *= al1 * fall_r;
                     oc[nt][2] *= al0;
                     oc[nt][3] *= al1;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        o[nt][j][0] *= al0 * fall;
-                        o[nt][j][1] *= al1 * fall;
-                        o[nt][j][2] *= al0 * fall;
-                        o[nt][j][3] *= al1 * fall;
+                        o[nt][j][0] *= al0 * fall[j / 2];
+                        o[nt][j][1] *= al1 * fall[j / 2];
+                        o[nt][j][2] *= al0 * fall[j / 2];
+                        o[nt][j][3] *= al1 * fall[j / 2];
                     }
                 }
                 E = e_new;
@@ -780,14 +792,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
             }
             constexpr float kUp = 16777216.0f;  // 2^24 of the codes
             constexpr float kUp1 = BITS == 4 ? kUp / 16.0f : kUp;
-            const float scale_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
+            const float own_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int hc = nt * 8 + 2 * t + c;
                 const float inv = oc[nt][2 + c] == 0.0f ? 0.0f : 1.0f / oc[nt][2 + c];  // 0: every score is -inf
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const float z = __shfl_sync(0xffffffffu, oc[nt][c], 4 * g + t);
+                    const float z = __shfl_sync(0xffffffffu, oc[nt][c], 4 * g + t), scale_e = __shfl_sync(0xffffffffu, own_e, g);
                     float* o0 = o[nt][2 * g];
                     float* o1 = o[nt][2 * g + 1];
                     if (BITS == 4) o0[c] -= o0[c + 2], o1[c] -= o1[c + 2];

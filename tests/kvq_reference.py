@@ -122,7 +122,7 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
     with u (1 + e), |e| <= 2^-11, the output moves by sum(p e (v - o)) at first order.  Half of the keys enter as
     hi - s (C - c), hi = lo + C s rounded to fp16 and C the greatest code; the product of u and s that weighs c or
     C - c is rounded to fp16 too: 2^-11 of sum(p (|hi| + s C)), which covers either.  fp16 steps end at 2^-24: as the
-    greatest u is at least 2^6 and lo, hi and s are scaled by the power of two above the greatest, M, each of n keys
+    greatest u is at least 2^6 and lo, hi and s are scaled by the power of two above the greatest of their group of dimensions, M, each of n keys
     adds at most 2^-25 / 2^6 (|v - o| + 2 M C), and the rounding of s, lo or hi itself 2^-25 * 2 M (C + 1) on average
     over the keys.  A code's low nibbles are summed as the difference of two sums up to 16 times as large: at most
     16 steps a warp at these tests' sizes, which may truncate (2^-23), 2^-14 of sum(p s C) in all.
@@ -152,7 +152,9 @@ def decode(q, kpool, vpool, table, lens, bits, scale):
                 o[b, h] = p @ v
                 top = 2 ** bits - 1
                 vhi, spread = np.abs(vlo + top * vs)[:, g], (top * vs)[:, g]
-                far, M = np.abs(v - o[b, h]), max(np.nanmax(vhi), np.nanmax(np.abs(vlo[:, g])), np.nanmax(vs[:, g]))
+                far = np.abs(v - o[b, h])
+                M = np.fmax(np.fmax(vhi, np.abs(vlo[:, g])), vs[:, g])
+                M = np.repeat(np.nanmax(M.reshape(n, -1, GROUP), (0, 2)), GROUP)
                 tol_o[b, h] = (1 + 2.0 ** -8) * (
                     2.0 ** -11 * (p @ far + p @ vhi) + (2.0 ** -11 + 2.0 ** -14) * (p @ spread)
                     + 2 * ex * (p @ (np.abs(vlo) + vs * vc)[:, g])

@@ -342,6 +342,24 @@ def test_decode_steps_of_one_sequence_differ_widely(cuda_device):
     check_decode(cuda_device, q, kpool, vpool, table, [n], bits, 0.125, dtypes=(torch.float32,))
 
 
+@pytest.mark.parametrize("d,bits,H", [(64, 4, 2), (64, 8, 9), (128, 4, 12), (128, 8, 1), (256, 4, 2), (256, 8, 3)])
+def test_decode_groups_of_dimensions_differ_widely(cuda_device, d, bits, H):
+    """Groups of 32 dimensions whose values are 2^8 to 2^60 apart and grow along the sequence: each is as exact as if alone."""
+    ps, lens = 16, [700, 90]
+    table, pages = make_table(lens, ps, 1, seed=6)
+    kpool, vpool = (ref.random_pool(pages, 1, ps, d, bits, seed=s) for s in (45, 46))
+    par = vpool.reshape(pages, -1, 16 * ref.row_bytes(d, bits))[..., 16 * d * bits // 8:]
+    f = np.ascontiguousarray(par).view(np.uint16).astype(np.uint32)
+    f = (f << 16).view(np.float32).reshape(pages, 1, 16, d // 32, 2)
+    f = f * 2.0 ** (-(60 // (d // 32 - 1)) * np.arange(d // 32)[::-1, None].astype(np.float64))
+    order = np.concatenate([table[b, :-(-n // ps)] for b, n in enumerate(lens)])
+    f[order] *= (2.0 ** (np.arange(len(order)) // 16))[:, None, None, None, None]
+    raw = (f.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    par[:] = raw.reshape(pages, -1).view(np.uint8).reshape(par.shape)
+    q = torch.randn(2, H, d, generator=torch.Generator().manual_seed(47)).to(torch.bfloat16)
+    check_decode(cuda_device, q, kpool, vpool, table, lens, bits, 0.1)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_decode_nan_rows(cuda_device, bits):
     """A NaN group in a valid key's K makes its head's outputs NaN; one in V the group's 32 columns only."""
