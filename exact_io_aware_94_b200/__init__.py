@@ -456,6 +456,8 @@ def _kvq_run(dev, stream, call):
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        elif stream.device_index != dev:
+            raise ValueError("the stream must be on device %d, as the tensors are" % dev)
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     if dev != torch.cuda.current_device():
@@ -531,8 +533,8 @@ def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None
     num_pages, Hkv, page_size, rows, max_blocks = _kvq_pools(dev, kpages, vpages, block_table, kv_lens, d, bits)
     if rows != B:
         raise ValueError("block_table must be [B, max_blocks]")
-    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != dev):
-        raise ValueError("ws must be a tensor on device %d" % dev)
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous()):
+        raise ValueError("ws must be a contiguous tensor on device %d" % dev)
 
     def call(handle):
         w = ws

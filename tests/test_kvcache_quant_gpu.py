@@ -500,6 +500,23 @@ def test_decode_streams_and_repeats(cuda_device):
     assert fa.fa_check_status() == fa.FA_OK
 
 
+def test_refused_streams_and_workspaces(cuda_device):
+    """A stream of another device, a workspace with gaps, one that is too small or misaligned: nothing is launched."""
+    dev, d, bits = cuda_device, 64, 4
+    with pytest.raises(ValueError, match="stream"):
+        fa._kvq_run(torch.cuda.current_device() + 1, torch.cuda.current_stream(), None)
+    kp, vp = fa.kvcache_quant_pages(2, 1, 16, d, bits, device=dev)
+    q, table, lens = torch.zeros(1, 1, d, dtype=torch.bfloat16, device=dev), i32([[0, 1]], dev), i32([20], dev)
+    n = fa.fa_decode_paged_quant_workspace_size(1, 1, 1, 2, 16, d, bits)
+    ws = torch.full((2, n + 256), 9, dtype=torch.uint8, device=dev)
+    for bad, error in ((ws[:, :n], ValueError), (ws[0, :n - 256], fa.FAError), (ws[0, 16:16 + n], fa.FAError),
+                       (torch.zeros(n, dtype=torch.uint8), ValueError)):
+        with pytest.raises(error):
+            fa.decode_paged_quant(q, kp, vp, table, lens, bits, ws=bad)
+    torch.cuda.synchronize()
+    assert (ws == 9).all() and fa.fa_check_status() == fa.FA_OK
+
+
 def test_decode_graphs_that_share_a_workspace(cuda_device):
     """Two captured graphs of different shapes with one workspace, replayed in turn with eager calls between them: each
     gives what its call alone gave, bit for bit, whatever the workspace held."""
