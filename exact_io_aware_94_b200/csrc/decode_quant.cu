@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may be set up while this one runs
+    kvq_wait_for_previous();
     Part* parts = reinterpret_cast<Part*>(smem + C::kMetaOff);
     float* part_lse = reinterpret_cast<float*>(smem + C::kLseOff);
     int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] exit, [1..4] first set, [8..] scan
@@ -903,7 +904,9 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
     __shared__ float4 s_o[kCombineThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x + 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel has ended and its writes are visible
+    // (No launch_dependents here: blocks of the next call's split kernel would be dealt out while this kernel's hold
+    // places, unevenly: 28 -> 34 us at 96 x 4,001 keys, 57 -> 71 us at 16 x 8,192.)
+    kvq_wait_for_previous();
     const int status = *static_cast<volatile const int*>(p.status);
     const int used = *p.used;
     const int4 cut = p.cut[i];
@@ -1021,18 +1024,9 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
     }
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1 + C::kVisit);
     const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
-    fa_decode_quant_split<D, BITS, NT><<<grid, kThreads, C::kBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || grid == 1) return e;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid - 1);
-    cfg.blockDim = dim3(kCombineThreads);
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_decode_quant_combine<D, BITS, NT>, p);
+    e = kvq_launch(fa_decode_quant_split<D, BITS, NT>, grid, kThreads, C::kBytes, stream, p);
+    if (e != cudaSuccess || grid == 1) return e;
+    return kvq_launch(fa_decode_quant_combine<D, BITS, NT>, grid - 1, kCombineThreads, 0, stream, p);
 }
 
 // 8-head tiles of a set: two (O takes NT D / 4 registers a thread) only where a second

@@ -219,6 +219,7 @@ template <int D, int BITS>
 __global__ void __launch_bounds__(kKvqThreads) fa_kvq_append(const KvqParams p) {
     using F = KvqFormat<D, BITS>;
     __shared__ long long s_tile[kKvqTokens];
+    kvq_wait_for_previous();
     if (*p.status == FA_ERR_TIMEOUT) return;
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
@@ -325,6 +326,7 @@ template <int D, int BITS, bool F32>
 __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p) {
     using F = KvqFormat<D, BITS>;
     __shared__ long long s_tile[kKvqTokens];
+    kvq_wait_for_previous();
     if (*p.status == FA_ERR_TIMEOUT) return;
     int b, first, n, pos0;
     if (!kvq_block(p, b, first, n, pos0)) return;
@@ -375,18 +377,17 @@ __global__ void __launch_bounds__(kKvqThreads) fa_kvq_read(const KvqParams p) {
     }
 }
 
+// launch(D, BITS) of the kernels for a head dimension and code width.
 template <typename F>
 cudaError_t by_format(int d, int bits, F&& launch) {
     if (bits == 4) {
-        if (d == 64) launch(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
-        else if (d == 128) launch(std::integral_constant<int, 128>(), std::integral_constant<int, 4>());
-        else launch(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
-    } else {
-        if (d == 64) launch(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
-        else if (d == 128) launch(std::integral_constant<int, 128>(), std::integral_constant<int, 8>());
-        else launch(std::integral_constant<int, 256>(), std::integral_constant<int, 8>());
+        if (d == 64) return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 4>());
+        if (d == 128) return launch(std::integral_constant<int, 128>(), std::integral_constant<int, 4>());
+        return launch(std::integral_constant<int, 256>(), std::integral_constant<int, 4>());
     }
-    return cudaGetLastError();
+    if (d == 64) return launch(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
+    if (d == 128) return launch(std::integral_constant<int, 128>(), std::integral_constant<int, 8>());
+    return launch(std::integral_constant<int, 256>(), std::integral_constant<int, 8>());
 }
 
 }  // namespace
@@ -436,7 +437,8 @@ extern "C" int fa_kvcache_append_quant(const void* k, const void* v, long long s
     p.max_blocks = max_blocks;
     p.chunks = static_cast<int>(chunks);
     const cudaError_t e = by_format(d, bits, [&](auto D, auto BITS) {
-        fa_kvq_append<D(), BITS()><<<static_cast<unsigned>(B * chunks), kKvqThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        return kvq_launch(fa_kvq_append<D(), BITS()>, static_cast<unsigned>(B * chunks), kKvqThreads, 0,
+                          static_cast<cudaStream_t>(stream), p);
     });
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -478,8 +480,8 @@ extern "C" int fa_kvcache_read_quant(const void* kpages, const void* vpages, con
     const cudaError_t e = by_format(d, bits, [&](auto D, auto BITS) {
         const unsigned grid = static_cast<unsigned>(B * chunks);
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
-        if (o_dtype == FA_DT_F32) fa_kvq_read<D(), BITS(), true><<<grid, kKvqThreads, 0, st>>>(p);
-        else fa_kvq_read<D(), BITS(), false><<<grid, kKvqThreads, 0, st>>>(p);
+        return o_dtype == FA_DT_F32 ? kvq_launch(fa_kvq_read<D(), BITS(), true>, grid, kKvqThreads, 0, st, p)
+                                    : kvq_launch(fa_kvq_read<D(), BITS(), false>, grid, kKvqThreads, 0, st, p);
     });
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -569,6 +569,64 @@ def attention64(q, kp, vp, table, lens, bits, scale, d):
     return o, lse, float(v.abs().max()), X
 
 
+def test_calls_behind_joins_and_copies(cuda_device):
+    """The calls behind what is no kernel of their stream (a fill, a copy, another stream's work), eagerly and captured:
+    each sees what was written before it.  A hundred steps back to back give what single steps give."""
+    dev, d, bits, H, Hkv, ps, n = cuda_device, 128, 4, 4, 2, 16, 600
+    table, pages = make_table([n, 40], ps, 1, seed=9)
+    td, lens = i32(table, dev), i32([n, 40], dev)
+    cu = i32([0, n, n + 40], dev)
+    gen = torch.Generator().manual_seed(130)
+    src = torch.randn(3, n + 40, 2, Hkv, d, generator=gen).to(torch.bfloat16).to(dev)
+    q = torch.randn(2, H, d, generator=gen).to(torch.bfloat16).to(dev)
+    qkv, now = torch.zeros_like(src[0]), torch.zeros_like(lens)
+    kp, vp = fa.kvcache_quant_pages(pages, Hkv, ps, d, bits, device=dev)
+    ws = fa.workspace(fa.fa_decode_paged_quant_workspace_size(2, H, Hkv, table.shape[1], ps, d, bits), dev)
+    side = torch.cuda.Stream(dev)
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            now.copy_(lens)                  # a copy, then the append on another stream
+            fa.kvcache_append_quant(qkv[:, 0], qkv[:, 1], kp, vp, cu, td, now, n, bits)
+        ws.zero_()                           # a fill, then a join
+        main.wait_stream(side)
+        a = fa.decode_paged_quant(q, kp, vp, td, now, bits, scale=0.1, ws=ws)
+        k, v = fa.kvcache_read_quant(kp, vp, cu, td, now, n + 40, n, Hkv, d, bits)
+        kp.zero_(), vp.zero_()               # the next step's pools hold nothing of this one's
+        return (*a, k, v)
+
+    want = []
+    for x in src:
+        qkv.copy_(x)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in step()])
+        torch.cuda.synchronize()
+    kn, vn = (ref.random_pool(pages, Hkv, ps, d, bits, seed=1) for _ in range(2))
+    c = src[0].float().cpu().numpy()
+    append_reference(kn, vn, c[:, 0], c[:, 1], [0, n, n + 40], table, [n, 40], bits)
+    o_ref, lse_ref, tol_o, tol_l = ref.decode(q.double().cpu().numpy(), kn, vn, table, [n, 40], bits, 0.1)
+    assert (np.abs(to_np(want[0][0]) - o_ref) <= tol_o + np.abs(o_ref) * 2.0 ** -23).all()
+    assert (np.abs(to_np(want[0][1]) - lse_ref) <= tol_l).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for mode in ("eager", "graph"):
+        got = []
+        for i in range(100):
+            qkv.copy_(src[i % 3])
+            if mode == "graph":
+                graph.replay()
+                got.append([t.clone() for t in out])
+            else:
+                got.append(step())
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert all(torch.equal(x, y) for x, y in zip(g, want[i % 3])), (mode, i)
+    assert fa.fa_check_status() == fa.FA_OK
+
+
 @pytest.mark.parametrize("lens,H,Hkv,ps,d,bits", [
     ([400000], 4, 1, 1024, 64, 4),                    # one long context over all CTAs
     ([90000, 3], 2, 2, 65536, 128, 8),                # the largest pages
