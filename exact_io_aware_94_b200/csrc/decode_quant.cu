@@ -38,10 +38,12 @@
 // which is what the cache's order of dimensions inside a token is for.
 //
 // Work.  A unit is a run of KT keys of one (sequence, KV head, head set).  To begin and end
-// a set costs a warp about as much as 96 keys, so a set counts as that many units more,
-// ahead of its own (batches with short sequences: 5 % of the time).  The units
+// a set costs a warp about as much as 64 keys, so a set counts as that many units more,
+// ahead of its own (batches with short sequences: 5 % of the time; 48 and 96 keys are within 2 % of it).  The units
 // of the whole batch, in that order, are cut into equal runs, one a CTA, and a CTA's run
-// into equal runs for its four warps.  A warp copies its units into a ring of S
+// into equal runs for its warps.  There is one CTA an SM: its warps advance together.
+// (Of three smaller CTAs on an SM the one that came first ran ahead, and the last one was left alone at the end: 203,
+// 230 and 264 us for the same work at 64 x 32,768 keys; one CTA ends at 244.)  A warp copies its units into a ring of S
 // stages of its own with 16-byte asynchronous copies (a 16-token tile of K or of V is
 // one run of bytes) and waits for no other warp: a set that lies in its run whole it
 // writes out itself.  A set that is cut at a warp's border leaves a part (normalised output and log-sum-exp) on
@@ -64,16 +66,13 @@
 namespace fa {
 namespace {
 
-constexpr int kMaxSms = 160;        // bounds the CTAs of a launch and so the workspace
-constexpr int NC = 4;               // warps of a CTA
-constexpr int kThreads = 32 * NC;
-// CTAs an SM holds: 4, 3 or 2 leave a thread 128, 168 or 255 registers, of which O alone
-// takes nt d / 4.  (One more with q in shared memory was no faster: 281 -> 289 us at d = 128, 48 -> 51 us at
-// d = 256.)  At d = 64 in 4 bits, three leave the shared memory for units of 64 keys.
-__host__ __device__ constexpr int ctas_per_sm(int d, int bits, int nt) {
-    return nt * d <= 64 && bits == 8 ? 4 : nt * d <= 128 ? 3 : 2;
+constexpr int kMaxSms = 160;  // CTAs of a launch, one an SM; bounds the workspace
+// Warps of a CTA: 16, 12 or 8 leave a thread 128, 168 or 255 registers, of which O alone
+// takes nt d / 4.  (Four more with q in shared memory were no faster: 281 -> 289 us at d = 128, 48 -> 51 us at
+// d = 256.)  At d = 64 in 4 bits, 12 leave the shared memory for units of 64 keys.
+__host__ __device__ constexpr int warps_of(int d, int bits, int nt) {
+    return nt * d <= 64 && bits == 8 ? 16 : nt * d <= 128 ? 12 : 8;
 }
-__host__ __device__ constexpr int max_ctas(int d, int bits, int nt) { return kMaxSms * ctas_per_sm(d, bits, nt); }
 constexpr float kRefBits = 6.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
 constexpr float kNoMax = -1e30f;    // the maximum of no score: finite, so that no difference is NaN
@@ -99,18 +98,19 @@ struct DecodeQuantParams {
 template <int D, int BITS, int NT>
 struct Cfg {
     using F = KvqFormat<D, BITS>;
-    static constexpr int kCtas = ctas_per_sm(D, BITS, NT);
-    static constexpr int kBudget = 228 * 1024 / kCtas - 1024;    // of a CTA
-    static constexpr int kFixed = NC * 8 * NT * D * 4 + 512;     // the warps' first parts
+    static constexpr int NC = warps_of(D, BITS, NT);
+    static constexpr int kBudget = 227 * 1024;
+    static constexpr int kFixed = NC * 8 * NT * D * 4 + NC * (64 + 8 * 8 * NT) + 256;  // the warps' first parts, what is kept of parts, the plan
+    static constexpr int kThreads = 32 * NC;
     // a warp's scores, parameters and stages of a unit of n tiles
     static constexpr int per_warp(int n, int stages) {
-        return 8 * NT * (16 * n + 4) * 4 + n * F::kGroups * 64 + 8 * NT * 8 + 64 + stages * 2 * n * F::kTileBytes;
+        return 8 * NT * (16 * n + 4) * 4 + n * F::kGroups * 64 + stages * 2 * n * F::kTileBytes;
     }
     // tiles of a unit: what is done once a unit is the smaller a part, the more it has
     static constexpr int kBlocks = D == 64 && kFixed + NC * per_warp(4, 2) <= kBudget ? 4 : kFixed + NC * per_warp(2, 2) <= kBudget ? 2 : 1;
     static constexpr int S = kFixed + NC * per_warp(kBlocks, 4) <= kBudget ? 4 : kFixed + NC * per_warp(kBlocks, 3) <= kBudget ? 3 : 2;
     static constexpr int KT = 16 * kBlocks;
-    static constexpr int kVisit = (96 + KT - 1) / KT;      // units that a set counts for beside its own
+    static constexpr int kVisit = (64 + KT - 1) / KT;      // units that a set counts for beside its own
     static constexpr int kHalf = kBlocks * F::kTileBytes;  // K (or V) of a stage
     static constexpr int kStageBytes = 2 * kHalf;
     static constexpr int HP = 8 * NT;  // heads of a set
@@ -132,7 +132,8 @@ struct Cfg {
     static constexpr int kLseOff = kMetaOff + NC * 2 * 32;             // [warp][first, last part][head], base 2
     static constexpr int kMiscOff = kLseOff + NC * 2 * HP * 4;
     static constexpr int kBytes = kMiscOff + 32 * 4;
-    static_assert(kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory of a CTA");
+    static_assert(NC <= 16, "a lane for each of the parts");
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
     static_assert(S >= 2, "a stage is copied while another is read");
     static_assert(HP * D * 4 <= kRingBytes, "a part fits a warp's ring");
 };
@@ -249,10 +250,11 @@ struct Part {
 };
 
 template <int D, int BITS, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
+__global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_quant_split(const __grid_constant__ DecodeQuantParams p) {
     using C = Cfg<D, BITS, NT>;
     using F = KvqFormat<D, BITS>;
     constexpr int KT = C::KT, kVisit = C::kVisit, S = C::S, HP = C::HP, NG = F::kGroups, PG = F::kPlaneGroups, NB = C::kBlocks;
+    constexpr int NC = C::NC, kThreads = C::kThreads;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");  // the combine kernel may be set up while this one runs
@@ -262,15 +264,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     int* misc = reinterpret_cast<int*>(smem + C::kMiscOff);  // [0] exit, [1..4] first set, [8..] scan
 
     // ---- plan: the number of units and the set of this CTA's first one
-    if (tid == 0) misc[0] = (atomicAdd(p.status, 0) == FA_ERR_TIMEOUT) ? 1 : 0;
+    if (tid == 0) misc[0] = *static_cast<volatile const int*>(p.status) == FA_ERR_TIMEOUT;
     const int HH = p.Hkv * p.sets;
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    int mine = 0;
+    int mine = 0, empty = 0;
     for (int b = b0; b < b1; ++b) {
         const int len = p.kv_lens[b];
         if (blockIdx.x == 0 && (len < 0 || len > p.cap)) atomicCAS(p.status, 0, FA_ERR_KV_LEN);
         mine += weight_of<KT, kVisit>(clamp_len(len, p.cap));
+        empty |= len <= 0;
     }
     int incl = mine;
 #pragma unroll
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         if (lane >= o) incl += up;
     }
     if (lane == 31) misc[8 + warp] = incl;
-    __syncthreads();
+    empty = __syncthreads_or(empty);
     if (misc[0]) {  // the combine kernel may see the status cleared by then
         if (tid == 0) {
             p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -294,13 +297,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         total += misc[8 + i];
     }
     const int U = total * HH;
-    // a CTA has a unit for each of its compute warps before another one is used
-    const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / NC));
+    // a CTA has a unit for each of its SM's four schedulers before another one is used
+    const int n_cta = max(1, min(static_cast<int>(gridDim.x), U / 4));
     const int cta = blockIdx.x;
     if (cta == 0 && tid == 0) *p.used = n_cta;
     if (cta >= n_cta) return;
     // sequences without keys
-    for (int b = cta; b < p.B; b += n_cta) {
+    for (int b = empty ? cta : p.B; b < p.B; b += n_cta) {
         if (p.kv_lens[b] > 0) continue;
         for (int i = tid; i < p.H * D; i += kThreads) {
             const size_t at = static_cast<size_t>(b) * p.H * D + i;
@@ -417,6 +420,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
     look_up();
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) issue();
+
+    if (tid == 0) {
+        // for the combine kernel: the set of the CTA's first place, if earlier units of the set are another CTA's
+        const int b = misc[1], hkv = misc[2] / p.sets, h_in = (misc[2] - hkv * p.sets) * HP, own = misc[3] + kVisit;
+        const int c0 = div_floor((own + 1LL) * n_cta - 1, U);
+        const int c1 = div_floor((own + static_cast<long long>(units_of<KT>(misc[4]))) * n_cta - 1, U);
+        p.cut[cta] = make_int4(b * p.H + hkv * group + h_in, min(HP, group - h_in), c0, u0 > own ? c1 - c0 + 1 : 0);
+    }
 
     // ---- the sets of this warp's run
     if (lane < 2) parts[2 * warp + lane].kind = 0;
@@ -823,74 +834,58 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, BITS, NT>::kCtas)) fa_decode
         at = end;
     }
 
-    if (tid == 0) {
-        // for the combine kernel: the set of the CTA's first place, if earlier units of the set are another CTA's
-        const int b = misc[1], hkv = misc[2] / p.sets, h_in = (misc[2] - hkv * p.sets) * HP, own = misc[3] + kVisit;
-        const int c0 = div_floor((own + 1LL) * n_cta - 1, U);
-        const int c1 = div_floor((own + static_cast<long long>(units_of<KT>(misc[4]))) * n_cta - 1, U);
-        p.cut[cta] = make_int4(b * p.H + hkv * group + h_in, min(HP, group - h_in), c0, u0 > own ? c1 - c0 + 1 : 0);
-    }
-
-    // ---- the CTA's parts: those of one set are neighbours in the order first, last of warp 0, first, last of warp 1, ...
+    // ---- the CTA's parts: in the order first, last of warp 0, first, last of warp 1, ... those of a set are neighbours.
+    // A set begins with a last part, or with the very first one if it begins before the CTA.  The warps share the sets out.
     __syncthreads();
-    const float* from[NC];
-    const float* from_lse[NC];
-    int n_from = 0;
-    bool before = false;
-    Part of{};
-    auto merge = [&](bool after) {
-        const int h_in = of.set * HP, G = min(HP, group - h_in);
-        const size_t head0 = static_cast<size_t>(of.b) * p.H + of.hkv * group + h_in;
-        const bool whole = !before && !after;
-        const size_t slot = static_cast<size_t>(2 * cta + (before ? 0 : 1)) * HP;
-        for (int e = tid; e < G * (D / 4); e += kThreads) {
-            const int h = e / (D / 4), d = e % (D / 4) * 4;
-            float M = -INFINITY, L = 0.0f;
-            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (i < n_from) M = fmaxf(M, from_lse[i][h]);
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                if (i >= n_from) break;
-                const float x = from_lse[i][h];
-                const float w = x == M ? 1.0f : ex2_approx(x - M);
-                const float4 y = *reinterpret_cast<const float4*>(from[i] + h * D + d);
-                L += w;
-                O.x = fmaf(w, y.x, O.x), O.y = fmaf(w, y.y, O.y), O.z = fmaf(w, y.z, O.z), O.w = fmaf(w, y.w, O.w);
-            }
-            const float inv = 1.0f / L;
-            O.x *= inv, O.y *= inv, O.z *= inv, O.w *= inv;
-            if (!whole) {
-                *reinterpret_cast<float4*>(p.part_o + (slot + h) * D + d) = O;
-                if (d == 0) p.part_lse[slot + h] = M + log2f(L);
-            } else {
-                if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + h) * D + d) = O;
-                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
-                    make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
-                if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
-            }
+    const int kind = lane < 2 * NC ? parts[lane].kind : 0;
+    const uint32_t any = __ballot_sync(0xffffffffu, kind != 0), ends = __ballot_sync(0xffffffffu, kind == 1) & 0x55555555u;
+    const uint32_t begins = any & (0xAAAAAAAAu | (any & (0u - any)));
+    const int n_sets = __popc(begins);
+    if (n_sets == 0) return;
+    const int mine_set = warp % n_sets, rank = warp / n_sets, ranks = (NC - 1 - mine_set) / n_sets + 1;
+    uint32_t from = begins;
+    for (int i = 0; i < mine_set; ++i) from &= from - 1;
+    const int i0 = __ffs(from) - 1;
+    from &= from - 1;
+    const uint32_t in = any & (0xFFFFFFFFu << i0) & (from ? (from & (0u - from)) - 1 : 0xFFFFFFFFu);  // its parts
+    const int n_in = (31 - __clz(in)) / 2 - i0 / 2 + 1;  // warps they are of, from warp i0 / 2 on: first parts but for the first of them
+    const bool before = i0 % 2 == 0, after = (in & ends) == 0, all = !before && !after;
+    const Part of = parts[i0];
+    const int h_in = of.set * HP, G = min(HP, group - h_in);
+    const size_t head0 = static_cast<size_t>(of.b) * p.H + of.hkv * group + h_in;
+    const size_t slot = static_cast<size_t>(2 * cta + (before ? 0 : 1)) * HP;
+    for (int e = rank * 32 + lane; e < G * (D / 4); e += ranks * 32) {
+        const int h = e / (D / 4), d = e % (D / 4) * 4;
+        float M = -INFINITY, L = 0.0f;
+        float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* lse = part_lse + h;
+        const float* first = first_part(i0 / 2) + h * D + d;
+        const float* y0 = before ? first : reinterpret_cast<const float*>(smem + C::kRingOff + i0 / 2 * C::kRingBytes) + h * D + d;
+        auto at = [&](int j) { return j ? (i0 & ~1) + 2 * j : i0; };
+#pragma unroll 4
+        for (int j = 0; j < n_in; ++j)
+            if (in >> at(j) & 1) M = fmaxf(M, lse[at(j) * HP]);
+#pragma unroll 4
+        for (int j = 0; j < n_in; ++j) {
+            const float x = lse[at(j) * HP];
+            const float4 y = *reinterpret_cast<const float4*>(j ? first + j * HP * D : y0);
+            if (!(in >> at(j) & 1)) continue;  // a warp without units
+            const float w = x == M ? 1.0f : ex2_approx(x - M);
+            L += w;
+            O.x = fmaf(w, y.x, O.x), O.y = fmaf(w, y.y, O.y), O.z = fmaf(w, y.z, O.z), O.w = fmaf(w, y.w, O.w);
         }
-        n_from = 0;
-        before = false;
-    };
-#pragma unroll
-    for (int w = 0; w < NC; ++w) {
-        const Part first = parts[2 * w], last = parts[2 * w + 1];
-        if (first.kind) {
-            if (n_from == 0) before = true;  // only warp 0's: the set starts before the CTA
-            of = first;
-            from[n_from] = first_part(w);
-            from_lse[n_from++] = part_lse + 2 * w * HP;
-            if (first.kind == 1) merge(false);
-        }
-        if (last.kind) {
-            of = last;
-            from[n_from] = reinterpret_cast<const float*>(smem + C::kRingOff + w * C::kRingBytes);
-            from_lse[n_from++] = part_lse + (2 * w + 1) * HP;
+        const float inv = 1.0f / L;
+        O.x *= inv, O.y *= inv, O.z *= inv, O.w *= inv;
+        if (!all) {
+            *reinterpret_cast<float4*>(p.part_o + (slot + h) * D + d) = O;
+            if (d == 0) p.part_lse[slot + h] = M + log2f(L);
+        } else {
+            if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + h) * D + d) = O;
+            else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
+                make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
+            if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
         }
     }
-    if (n_from) merge(true);
 }
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
@@ -900,7 +895,7 @@ constexpr int kCombineThreads = 256;
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
     constexpr int HP = 8 * NT, D4 = D / 4;
-    __shared__ float s_w[HP][max_ctas(D, BITS, NT)];  // of part c0 + i, normalised
+    __shared__ float s_w[HP][kMaxSms];  // of part c0 + i, normalised
     __shared__ float4 s_o[kCombineThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x + 1;
@@ -1023,8 +1018,8 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1 + C::kVisit);
-    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(C::kCtas * std::min(kMaxSms, num_sms), units / NC)));
-    e = kvq_launch(fa_decode_quant_split<D, BITS, NT>, grid, kThreads, C::kBytes, stream, p);
+    const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxSms, num_sms), units / 4)));
+    e = kvq_launch(fa_decode_quant_split<D, BITS, NT>, grid, C::kThreads, C::kBytes, stream, p);
     if (e != cudaSuccess || grid == 1) return e;
     return kvq_launch(fa_decode_quant_combine<D, BITS, NT>, grid - 1, kCombineThreads, 0, stream, p);
 }
@@ -1039,7 +1034,7 @@ struct Workspace {
 };
 Workspace workspace_of(int H, int Hkv, int d, int bits) {
     const int nt = tiles_of(H / Hkv, d);
-    const size_t ctas = max_ctas(d, bits, nt), heads = 8 * nt;
+    const size_t ctas = kMaxSms, heads = 8 * nt;
     Workspace w{};
     w.lse = up256(2 * ctas * heads * d * sizeof(float));
     w.cut = w.lse + up256(2 * ctas * heads * sizeof(float));
