@@ -835,55 +835,57 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
     }
 
     // ---- the CTA's parts: in the order first, last of warp 0, first, last of warp 1, ... those of a set are neighbours.
-    // A set begins with a last part, or with the very first one if it begins before the CTA.  The warps share the sets out.
+    // A set begins with a last part, or with the very first one if it begins before the CTA: NC + 1 sets at most.  The
+    // warps share them out.
     __syncthreads();
     const int kind = lane < 2 * NC ? parts[lane].kind : 0;
     const uint32_t any = __ballot_sync(0xffffffffu, kind != 0), ends = __ballot_sync(0xffffffffu, kind == 1) & 0x55555555u;
     const uint32_t begins = any & (0xAAAAAAAAu | (any & (0u - any)));
-    const int n_sets = __popc(begins);
-    if (n_sets == 0) return;
-    const int mine_set = warp % n_sets, rank = warp / n_sets, ranks = (NC - 1 - mine_set) / n_sets + 1;
-    uint32_t from = begins;
-    for (int i = 0; i < mine_set; ++i) from &= from - 1;
-    const int i0 = __ffs(from) - 1;
-    from &= from - 1;
-    const uint32_t in = any & (0xFFFFFFFFu << i0) & (from ? (from & (0u - from)) - 1 : 0xFFFFFFFFu);  // its parts
-    const int n_in = (31 - __clz(in)) / 2 - i0 / 2 + 1;  // warps they are of, from warp i0 / 2 on: first parts but for the first of them
-    const bool before = i0 % 2 == 0, after = (in & ends) == 0, all = !before && !after;
-    const Part of = parts[i0];
-    const int h_in = of.set * HP, G = min(HP, group - h_in);
-    const size_t head0 = static_cast<size_t>(of.b) * p.H + of.hkv * group + h_in;
-    const size_t slot = static_cast<size_t>(2 * cta + (before ? 0 : 1)) * HP;
-    for (int e = rank * 32 + lane; e < G * (D / 4); e += ranks * 32) {
-        const int h = e / (D / 4), d = e % (D / 4) * 4;
-        float M = -INFINITY, L = 0.0f;
-        float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* lse = part_lse + h;
-        const float* first = first_part(i0 / 2) + h * D + d;
-        const float* y0 = before ? first : reinterpret_cast<const float*>(smem + C::kRingOff + i0 / 2 * C::kRingBytes) + h * D + d;
+    const int n_sets = __popc(begins), at_once = min(n_sets, NC);
+    for (int k = n_sets ? warp % at_once : 1; k < n_sets; k += NC) {
+        const int rank = warp / at_once, ranks = (NC - 1 - warp % at_once) / at_once + 1;
+        uint32_t from = begins;
+        for (int i = 0; i < k; ++i) from &= from - 1;
+        const int i0 = __ffs(from) - 1;
+        from &= from - 1;
+        const uint32_t in = any & (0xFFFFFFFFu << i0) & (from ? (from & (0u - from)) - 1 : 0xFFFFFFFFu);  // its parts
+        const int n_in = (31 - __clz(in)) / 2 - i0 / 2 + 1;  // the warps from i0 / 2 on: first parts, but for the first one's
+        const bool before = i0 % 2 == 0, after = (in & ends) == 0, whole = !before && !after;
+        const Part of = parts[i0];
+        const int h_in = of.set * HP, G = min(HP, group - h_in);
+        const size_t head0 = static_cast<size_t>(of.b) * p.H + of.hkv * group + h_in;
+        const size_t slot = static_cast<size_t>(2 * cta + (before ? 0 : 1)) * HP;
         auto at = [&](int j) { return j ? (i0 & ~1) + 2 * j : i0; };
+        for (int e = rank * 32 + lane; e < G * (D / 4); e += ranks * 32) {
+            const int h = e / (D / 4), d = e % (D / 4) * 4;
+            float M = -INFINITY, L = 0.0f;
+            float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float* lse = part_lse + h;
+            const float* first = first_part(i0 / 2) + h * D + d;
+            const float* y0 = before ? first : reinterpret_cast<const float*>(smem + C::kRingOff + i0 / 2 * C::kRingBytes) + h * D + d;
 #pragma unroll 4
-        for (int j = 0; j < n_in; ++j)
-            if (in >> at(j) & 1) M = fmaxf(M, lse[at(j) * HP]);
+            for (int j = 0; j < n_in; ++j)
+                if (in >> at(j) & 1) M = fmaxf(M, lse[at(j) * HP]);
 #pragma unroll 4
-        for (int j = 0; j < n_in; ++j) {
-            const float x = lse[at(j) * HP];
-            const float4 y = *reinterpret_cast<const float4*>(j ? first + j * HP * D : y0);
-            if (!(in >> at(j) & 1)) continue;  // a warp without units
-            const float w = x == M ? 1.0f : ex2_approx(x - M);
-            L += w;
-            O.x = fmaf(w, y.x, O.x), O.y = fmaf(w, y.y, O.y), O.z = fmaf(w, y.z, O.z), O.w = fmaf(w, y.w, O.w);
-        }
-        const float inv = 1.0f / L;
-        O.x *= inv, O.y *= inv, O.z *= inv, O.w *= inv;
-        if (!all) {
-            *reinterpret_cast<float4*>(p.part_o + (slot + h) * D + d) = O;
-            if (d == 0) p.part_lse[slot + h] = M + log2f(L);
-        } else {
-            if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + h) * D + d) = O;
-            else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
-                make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
-            if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+            for (int j = 0; j < n_in; ++j) {
+                const float x = lse[at(j) * HP];
+                const float4 y = *reinterpret_cast<const float4*>(j ? first + j * HP * D : y0);
+                if (!(in >> at(j) & 1)) continue;  // a warp without units
+                const float w = x == M ? 1.0f : ex2_approx(x - M);
+                L += w;
+                O.x = fmaf(w, y.x, O.x), O.y = fmaf(w, y.y, O.y), O.z = fmaf(w, y.z, O.z), O.w = fmaf(w, y.w, O.w);
+            }
+            const float inv = 1.0f / L;
+            O.x *= inv, O.y *= inv, O.z *= inv, O.w *= inv;
+            if (!whole) {
+                *reinterpret_cast<float4*>(p.part_o + (slot + h) * D + d) = O;
+                if (d == 0) p.part_lse[slot + h] = M + log2f(L);
+            } else {
+                if (p.o_dtype == FA_DT_F32) *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (head0 + h) * D + d) = O;
+                else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (head0 + h) * D + d) =
+                    make_uint2(pack_bf16x2(O.x, O.y), pack_bf16x2(O.z, O.w));
+                if (d == 0) p.lse[head0 + h] = (M + log2f(L)) * 0.6931471805599453f;
+            }
         }
     }
 }

@@ -657,6 +657,15 @@ def test_decode_sizes(cuda_device, lens, H, Hkv, ps, d, bits):
     assert (o[zero] == 0).all()
 
 
+@pytest.mark.parametrize("d,bits,H,warps", [(64, 4, 1, 12), (64, 8, 4, 16), (128, 4, 4, 12), (128, 8, 2, 12), (256, 4, 2, 8),
+                                            (256, 8, 1, 8), (128, 4, 12, 8), (64, 8, 12, 12)])
+def test_decode_sequences_about_as_long_as_a_warps_run(cuda_device, d, bits, H, warps):
+    """Equal sequences, 2 % more of them than the GPU's warps: every warp's border cuts one, so a block of `warps` warps
+    begins and ends with a part and merges a set more than it has warps."""
+    n = torch.cuda.get_device_properties(cuda_device).multi_processor_count * warps * 102 // 100
+    test_decode_sizes(cuda_device, [320] * n, H, 1, 64, d, bits)
+
+
 def test_nothing_is_written_after_a_timeout(cuda_device):
     """Once a wait anywhere in the library has run out (the fault-injection build), the calls write nothing until
     fa_check_status has returned that."""
