@@ -627,6 +627,47 @@ def test_calls_behind_joins_and_copies(cuda_device):
     assert fa.fa_check_status() == fa.FA_OK
 
 
+def test_default_stream_waits_for_blocking_streams(cuda_device):
+    """The legacy default stream waits for a blocking stream's work without an event, and that stream for the default
+    stream's: the calls keep to it."""
+    import ctypes
+
+    cudart = torch.cuda.cudart()
+    handle = ctypes.c_void_p()
+    assert int(cudart.cudaStreamCreate(ctypes.addressof(handle))) == 0
+    other = torch.cuda.ExternalStream(handle.value, device=cuda_device)
+    dev, d, bits, H, Hkv, ps, n = cuda_device, 128, 4, 4, 2, 16, 500
+    table, pages = make_table([n], ps, 1, seed=19)
+    td, lens, cu = i32(table, dev), i32([n], dev), i32([0, n], dev)
+    gen = torch.Generator().manual_seed(140)
+    src = torch.randn(3, 2, n, Hkv, d, generator=gen).to(torch.bfloat16).to(dev)
+    q = torch.randn(1, H, d, generator=gen).to(torch.bfloat16).to(dev)
+    kp, vp = fa.kvcache_quant_pages(pages, Hkv, ps, d, bits, device=dev)
+    delay = torch.randn(4096, 4096, device=dev)
+
+    def step(i):
+        with torch.cuda.stream(other):
+            for _ in range(3):
+                torch.mm(delay, delay)
+            fa.kvcache_append_quant(src[i, 0], src[i, 1], kp, vp, cu, td, lens, n, bits)
+        o, lse = fa.decode_paged_quant(q, kp, vp, td, lens, bits, scale=0.1)
+        with torch.cuda.stream(other):
+            kp.zero_(), vp.zero_()
+        return o, lse
+
+    want = []
+    for i in range(3):
+        want.append([t.clone() for t in step(i)])
+        torch.cuda.synchronize()
+    assert all(float((want[0][0] - w[0]).abs().max()) > 0.01 for w in want[1:])
+    got = [step(i % 3) for i in range(30)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 3])), i
+    assert fa.fa_check_status() == fa.FA_OK
+    assert int(cudart.cudaStreamDestroy(handle.value)) == 0
+
+
 @pytest.mark.parametrize("lens,H,Hkv,ps,d,bits", [
     ([400000], 4, 1, 1024, 64, 4),                    # one long context over all CTAs
     ([90000, 3], 2, 2, 65536, 128, 8),                # the largest pages
