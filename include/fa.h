@@ -297,7 +297,7 @@ int fa_kvcache_read_quant(const void* kpages, const void* vpages, const int* cu_
                           const int* kv_lens, void* k_out, void* v_out, int B, int H, int Hkv, int total, int max_seqlen,
                           int num_pages, int page_size, int max_blocks, int d, int bits, int o_dtype, void* stream);
 
-/* Workspace bytes fa_decode_paged_quant needs; 0 for invalid arguments. */
+/* Workspace bytes fa_decode_paged_quant needs (256-byte aligned, not initialised); 0 for invalid arguments. */
 size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits);
 
 /*
