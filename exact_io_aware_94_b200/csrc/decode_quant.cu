@@ -17,8 +17,10 @@
 //
 // Weights.  u = 2^6 2^(x - m), below 2^14 because the reference m follows the maximum to
 // within 8 bits, is rounded to fp16 (11 bits; bf16 has 8) once for a key and head, and
-// u s again.  s and the offsets are scaled by 2^-E, which keeps those of every unit below 2; each group of dimensions has
-// an E of its own, so that one with large values takes nothing from the others.
+// u s again.  The offsets are scaled by 2^-E and s, which a group's range has 2^BITS - 1 times, by 2^(BITS - 1 - E): that
+// keeps those of every unit below 2, and u s below 2^15.  Each group of dimensions has an E of its own, so that one with large
+// values takes nothing from the others.  fp16 ends at 2^-24, so a value is off by at most 2^-25 2^E for its offset and twice
+// that for s: beside a token whose values in the group are 2^13 times larger it has bf16's digits left.
 // One product of the rounded u with [offset of each group; ones] gives the sums of u times the offset
 // and of u: the output is divided by the sum of the same rounded weights, so their errors only weigh values against
 // each other.  lse takes the fp32 sum.
@@ -115,7 +117,8 @@ struct Cfg {
     static constexpr int kStageBytes = 2 * kHalf;
     static constexpr int HP = 8 * NT;  // heads of a set
     static constexpr int kScoreStride = KT + 4;
-    // V's s and offsets of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], offset [tile][group][key % 4][key / 4]
+    static constexpr int kSUp = BITS - 1;  // s is held times 2^kSUp
+    // V's s 2^kSUp and offsets of a unit over 2^E in fp16: s [tile][key % 4][group][key / 4], offset [tile][group][key % 4][key / 4]
     static constexpr int kSBytes = kBlocks * F::kGroups * 32;
     static constexpr int kPairs = kBlocks * F::kGroups / 4;  // pairs of keys of a group that a thread converts
     static_assert(kPairs > 0, "a unit has a pair for every thread");
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
         float oc[NT][4];  // heads 2 t, 2 t + 1: sums of u times the offset of group r, sums of u
         float m[NT], l[NT];
         int E = -100;                      // of group pair_group
-        float down = 0.0f, s_down = 0.0f;  // 2^-E, and that with the sign of s in this thread's pairs
+        float down = 0.0f, s_down = 0.0f;  // 2^-E, and 2^(kSUp - E) with the sign of s in this thread's pairs
         // q as the B operand: thread (head r, t) holds dimensions 32 g + 8 t + [0, 8)
         uint32_t qb[NT][NG][4];
         uint32_t qz[NT][C::kZSteps][2];  // sums of q over a group, as the B operand of the lo product
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                     row[C::kScoreStride + 2] = fmaf(x1[nt][3], A[nt][1], x2[nt][3]);
                 }
             }
-            // V's parameters over 2^E: a thread converts those of a group of two keys, 4 apart, for each i.
+            // V's parameters as the products want them: a thread converts those of a group of two keys, 4 apart, for each i.
             // fp16 bit 14 tells a value of 2 or more, an infinity or NaN: then E has to be looked at below.
             uint32_t over = 0;
             auto convert = [&]() {
@@ -663,16 +666,16 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                 grow |= mx[nt] > m[nt] + kGrowBits;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                uint32_t top = 0;  // greatest magnitude of the group's parameters in the unit, as fp32 bits; NaN left out
+                uint32_t top = 0;  // greatest magnitude of the group's s 2^kSUp and offsets in the unit, as fp32 bits; NaN left out
 #pragma unroll
                 for (int i = 0; i < C::kPairs; ++i)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t w = *reinterpret_cast<const uint32_t*>(
                             vs + (pair_of(i) / 8) * F::kTileBytes + F::kParamOff + (pair_key(i) + 4 * x) * F::kParamBytes + pair_group * 4);
-                        const uint32_t hi = w & 0x7FFF0000u;
-                        const uint32_t lo = __float_as_uint(fmaf(s_of(w), to_offset, lo_of(w))) & 0x7FFFFFFFu;
-                        top = max(top, max(hi < 0x7F800000u ? hi : 0u, lo < 0x7F800000u ? lo : 0u));
+                        const uint32_t step = __float_as_uint(s_of(w) * static_cast<float>(1 << C::kSUp)) & 0x7FFFFFFFu;
+                        const uint32_t off = __float_as_uint(fmaf(s_of(w), to_offset, lo_of(w))) & 0x7FFFFFFFu;
+                        top = max(top, max(step < 0x7F800000u ? step : 0u, off < 0x7F800000u ? off : 0u));
                     }
 #pragma unroll
                 for (int x = NG; x < 32; x *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                 }
                 E = e_new;
                 down = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);  // 2^-E
-                s_down = complement ? -down : down;
+                s_down = (complement ? -down : down) * static_cast<float>(1 << C::kSUp);
                 __syncwarp();  // the scores have been read: not before the parameters are written anew
                 convert();
             }
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                 if (whole) p.lse[head0 + h] = lse * 0.6931471805599453f;
                 else part_lse[(2 * warp + (before ? 0 : 1)) * HP + h] = lse;
             }
-            constexpr float kUp = 16777216.0f;  // 2^24 of the codes
+            constexpr float kUp = static_cast<float>(1 << (24 - C::kSUp));  // 2^24 of the codes, less that of s
             constexpr float kUp1 = BITS == 4 ? kUp / 16.0f : kUp;
             const float own_e = __uint_as_float(static_cast<uint32_t>(127 + E) << 23);
 #pragma unroll

@@ -306,10 +306,11 @@ size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_block
  * o [B, H, d] (o_dtype), lse [B, H] fp32, and the device-side conditions
  * (FA_ERR_KV_LEN, FA_ERR_PAGE, a length of 0) are those of fa_decode_paged.
  * What a page holds past a sequence's length never changes a result.
- * The weights of the values are rounded to fp16 (2^-11 of each term); an output is
- * as exact as that beside the largest magnitude that its group of FA_KVQ_GROUP
- * dimensions takes in the sequence's V, not beside itself: values 2^20 times
- * smaller than another token's in the same group lose their own digits.
+ * The weights of the values are rounded to fp16 (2^-11 of each term).  A value's
+ * own error is at most 2^-22 of the largest magnitude that its group of
+ * FA_KVQ_GROUP dimensions takes in the sequence's V, whatever the weights: values
+ * 2^13 times smaller than another token's in the same group are held to 2^-9 of
+ * themselves, those 2^22 times smaller are lost beside it.
  */
 int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
                           const int* kv_lens, void* o, float* lse, int B, int H, int Hkv, int num_pages, int page_size,

@@ -1,0 +1,86 @@
+"""Decode over the quantised paged cache where outputs are small beside the largest values."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_94_b200 as fa
+
+from . import kvq_reference as ref
+from . import test_kvcache_quant_gpu as kvq
+from .parity import to_np
+
+pytestmark = pytest.mark.gpu
+
+
+def decode64(q, kpool, vpool, table, lens, bits, scale):
+    """(o, tolerance of o) in 64 bits for q [B, H, d] (float64).
+
+    Tolerances.  A key's weight u is 2^6 or more for the greatest p of its warp's keys.  It is rounded to fp16, and the output
+    is divided by the sum of the rounded weights: p moves by 2^-11 p + min(p, 2^-25 / 2^6 of the greatest p), which weighs
+    v - o.  The offset of a group, lo or hi = lo + C s (C the greatest code), is rounded to fp16 over 2^E: by 2^-11 of it or
+    2^-25 2^E, whichever is more.  s is held over 2^(E - bits + 1), exactly or to 2^-25 of that, and multiplies c or C - c,
+    at most C; u s is rounded to fp16 likewise, by 2^-11 or 2^-31 2^(E - bits + 1) of the greatest p.  2^E is at most twice
+    M, the greatest of |lo|, |hi| and 2^(bits - 1) s that the group of dimensions has in the sequence.  Scores are off by
+    2^-20 of the sum of their terms' magnitudes, exponentials by 2^-22.  Sums of low nibbles may lose 2^-14 of sum(p s C).
+    1 + 2^-8 covers the products of these."""
+    B, H, d = q.shape
+    G, C, half = H // kpool.shape[1], 2 ** bits - 1, 2.0 ** (bits - 1)
+    o, tol = np.zeros((B, H, d)), np.zeros((B, H, d))
+    for b in range(B):
+        n = int(lens[b])
+        kc, klo, ks = ref.rows(kpool, table[b], range(n), d, bits, ref.K_UNIT)
+        vc, vlo, vs = ref.rows(vpool, table[b], range(n), d, bits, ref.V_UNIT)
+        for h in range(H):
+            g = h // G
+            x = scale * ((klo + ks * kc)[:, g] @ q[b, h])
+            ex = 2.0 ** -20 * scale * ((np.abs(klo) + ks * kc)[:, g] @ np.abs(q[b, h])).max() + 2.0 ** -21
+            p = np.exp(x - x.max())
+            p /= p.sum()
+            lo, s, c = vlo[:, g], vs[:, g], vc[:, g]
+            v, hi = lo + s * c, lo + C * s
+            o[b, h] = p @ v
+            big = np.maximum(np.abs(lo), np.abs(hi))
+            M = np.maximum(big, half * s).reshape(n, -1, ref.GROUP).max((0, 2)).repeat(ref.GROUP)
+            least = np.minimum(p, 2.0 ** -31 * p.max())[:, None]
+            tol[b, h] = (1 + 2.0 ** -8) * (
+                ((2.0 ** -11 * p)[:, None] + least).T.reshape(1, n) @ np.abs(v - o[b, h])
+                + p @ np.maximum(2.0 ** -11 * big, 2.0 ** -25 * 2 * M)
+                + (2.0 ** -11 + 2.0 ** -14) * (p @ (C * s)) + 2.0 ** -25 * 2 * M * C / half
+                + np.minimum(p[:, None] * s * C, 2.0 ** -31 * p.max() * 2 * M * C / half).sum(0)
+                + 2 * ex * (p @ (np.abs(lo) + s * c)))[0]
+    return o, tol
+
+
+@pytest.mark.parametrize("log2_ratio", [0, 6, 8, 10, 12, 14])
+@pytest.mark.parametrize("d,bits,H,Hkv", [(64, 4, 3, 1), (64, 8, 9, 1), (128, 4, 12, 1), (128, 8, 4, 2), (256, 4, 2, 1),
+                                          (256, 8, 8, 1)])
+def test_decode_beside_large_values_without_weight(cuda_device, d, bits, H, Hkv, log2_ratio):
+    """One token of every 16 has values 2^log2_ratio times those of the others and a score some 40 nats below: the output
+    is the others' average, and nearly as exact as without that token.  A bound below 2^-6 of every output shows that
+    zeros, or the small values' codes lost, would not pass."""
+    dev, ps, lens = cuda_device, 16, [64, 33, 700]
+    table, pages = kvq.make_table(lens, ps, 1, seed=3)
+    gen = torch.Generator().manual_seed(150 + log2_ratio)
+    T = sum(lens)
+    q = torch.randn(len(lens), H, d, generator=gen).abs().to(torch.bfloat16)
+    k = 0.1 * torch.randn(T, Hkv, d, generator=gen)
+    sign = torch.where(torch.rand(Hkv, d, generator=gen) < 0.5, -1.0, 1.0)
+    v = (1.0 + 0.4 * torch.randn(T, Hkv, d, generator=gen).clamp(-2, 2)) * sign
+    at = torch.arange(T)
+    loud = at % 16 == at // 16 * 5 % 16
+    k[loud] -= 5.0 * math.sqrt(128.0 / d)
+    v[loud] *= 2.0 ** log2_ratio
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    kpool, vpool = (np.zeros((pages, Hkv, ps * ref.row_bytes(d, bits)), np.uint8) for _ in range(2))
+    cu = np.concatenate(([0], np.cumsum(lens)))
+    kvq.append_reference(kpool, vpool, k.float().numpy(), v.float().numpy(), cu, table, lens, bits)
+    scale = 1.0 / math.sqrt(d)
+    o_ref, tol = decode64(q.double().numpy(), kpool, vpool, table, lens, bits, scale)
+    assert (tol <= 2.0 ** -6 * np.abs(o_ref)).all()
+    o, _ = fa.decode_paged_quant(q.to(dev), torch.from_numpy(kpool).to(dev), torch.from_numpy(vpool).to(dev),
+                                 kvq.i32(table, dev), kvq.i32(lens, dev), bits, scale=scale)
+    assert fa.fa_check_status() == fa.FA_OK
+    over = np.abs(to_np(o) - o_ref) / tol
+    assert over.max() <= 1.0, "o beyond its tolerance by a factor of %.3g" % over.max()
