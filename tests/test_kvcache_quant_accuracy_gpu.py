@@ -1,4 +1,5 @@
-"""Decode over the quantised paged cache where outputs are small beside the largest values."""
+"""Decode over the quantised paged cache where outputs are small beside the largest values: tokens of widely different
+magnitudes, long sequences, the largest pages."""
 import math
 
 import numpy as np
@@ -84,3 +85,34 @@ def test_decode_beside_large_values_without_weight(cuda_device, d, bits, H, Hkv,
     assert fa.fa_check_status() == fa.FA_OK
     over = np.abs(to_np(o) - o_ref) / tol
     assert over.max() <= 1.0, "o beyond its tolerance by a factor of %.3g" % over.max()
+
+
+@pytest.mark.parametrize("lens,H,Hkv,ps,d,bits", [
+    ([400000], 4, 1, 1024, 64, 4),
+    ([400000], 2, 1, 1024, 64, 8),
+    ([90000, 3], 2, 2, 65536, 128, 8),
+    ([70000, 65536, 65537], 12, 1, 65536, 128, 4),
+    ([66000, 131072], 9, 1, 65536, 64, 4),
+    ([70000], 3, 1, 65536, 256, 4),
+    ([16, 70000], 2, 2, 65536, 256, 8),
+])
+def test_decode_outputs_of_long_sequences(cuda_device, lens, H, Hkv, ps, d, bits):
+    """Each head's error beside its output, in the norm: the roundings of a key (fp16, 2^-12.8 in the mean square, of the
+    weight, the offset and the weighted step: terms of at most 4 standard deviations of a value) are independent, and over many
+    keys average out as the values do.  They are sqrt(3) 4 2^-12.8 = 2^-10 of an output; 2^-8 leaves a factor of 4.  Values of another page, or
+    zeros, would be off by the whole output."""
+    dev = cuda_device
+    table, pages = kvq.make_table(lens, ps, 2, seed=9)
+    kd, vd = (torch.from_numpy(ref.random_pool(pages, Hkv, ps, d, bits, seed=160 + i)).to(dev) for i in (0, 1))
+    q = torch.randn(len(lens), H, d, generator=torch.Generator().manual_seed(161)).to(torch.bfloat16).to(dev)
+    table, lens = kvq.i32(table, dev), kvq.i32(lens, dev)
+    o_ref, _, _, _ = kvq.attention64(q, kd, vd, table, lens, bits, 1.0 / math.sqrt(d), d)
+    o, _ = fa.decode_paged_quant(q, kd, vd, table, lens, bits)
+    assert fa.fa_check_status() == fa.FA_OK
+    off = (o - o_ref).norm(dim=-1) / o_ref.norm(dim=-1)
+    assert float(off.max()) <= 2.0 ** -8, "off by %.3g of the output" % float(off.max())
+
+
+@pytest.mark.parametrize("d,bits,H,Hkv", [(64, 8, 1, 1), (64, 8, 9, 1), (128, 8, 12, 1)])
+def test_decode_average_of_many_values_in_the_other_formats(cuda_device, d, bits, H, Hkv):
+    kvq.test_decode_average_of_many_values(cuda_device, d, bits, H, Hkv)
