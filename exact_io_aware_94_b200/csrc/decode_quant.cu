@@ -60,6 +60,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "kvquant.cuh"
@@ -1010,6 +1011,14 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
     }
 }
 
+// What a batch of full sequences counts for.  The kernels count in int32, a little past the last unit too.
+template <int D, int BITS, int NT>
+long long units_at_capacity(int B, int Hkv, int sets, int cap) {
+    using C = Cfg<D, BITS, NT>;
+    return static_cast<long long>(B) * Hkv * sets * ((cap - 1) / C::KT + 1 + C::kVisit);
+}
+constexpr long long kMaxUnits = 0x7FFFFF00LL;
+
 template <int D, int BITS, int NT>
 cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_t stream) {
     using C = Cfg<D, BITS, NT>;
@@ -1022,7 +1031,7 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
             return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const long long units = static_cast<long long>(p.B) * p.Hkv * p.sets * ((p.cap - 1) / C::KT + 1 + C::kVisit);
+    const long long units = units_at_capacity<D, BITS, NT>(p.B, p.Hkv, p.sets, p.cap);
     const int grid = static_cast<int>(std::max(1LL, std::min<long long>(std::min(kMaxSms, num_sms), units / 4)));
     e = kvq_launch(fa_decode_quant_split<D, BITS, NT>, grid, C::kThreads, C::kBytes, stream, p);
     if (e != cudaSuccess || grid == 1) return e;
@@ -1032,12 +1041,37 @@ cudaError_t launch(const DecodeQuantParams& p, int dev, int num_sms, cudaStream_
 // 8-head tiles of a set: two (O takes NT D / 4 registers a thread) only where a second
 // one has heads, and D leaves room for it.
 int tiles_of(int group, int d) { return d <= 128 && group > 8 ? 2 : 1; }
+int sets_of(int group, int nt) { return (group - 1) / (8 * nt) + 1; }
+
+// f(D, BITS, NT) of the kernels for a head dimension, code width and number of tiles.
+template <typename F>
+auto by_kernel(int d, int bits, int nt, F&& f) {
+    auto with_bits = [&](auto D, auto NT) {
+        return bits == 4 ? f(D, std::integral_constant<int, 4>(), NT) : f(D, std::integral_constant<int, 8>(), NT);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (d == 256) return with_bits(std::integral_constant<int, 256>(), One());
+    if (d == 128) return nt == 1 ? with_bits(std::integral_constant<int, 128>(), One()) : with_bits(std::integral_constant<int, 128>(), Two());
+    return nt == 1 ? with_bits(std::integral_constant<int, 64>(), One()) : with_bits(std::integral_constant<int, 64>(), Two());
+}
+
+// kvq_check_pool, and whether the batch at its capacity can be counted.
+int check_sizes(int B, int H, int Hkv, int num_pages, int page_size, int max_blocks, int d, int bits) {
+    const int rc = kvq_check_pool(B, H, Hkv, num_pages, page_size, max_blocks, d, bits);
+    if (rc != FA_OK) return rc;
+    const int nt = tiles_of(H / Hkv, d);
+    const long long units = by_kernel(d, bits, nt, [&](auto D, auto BITS, auto NT) {
+        return units_at_capacity<D(), BITS(), NT()>(B, Hkv, sets_of(H / Hkv, nt), max_blocks * page_size);
+    });
+    return units > kMaxUnits ? FA_ERR_INVALID_ARG : FA_OK;
+}
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct Workspace {
     size_t lse, cut, used, total;  // offsets of the arrays after part_o
 };
-Workspace workspace_of(int H, int Hkv, int d, int bits) {
+Workspace workspace_of(int H, int Hkv, int d) {
     const int nt = tiles_of(H / Hkv, d);
     const size_t ctas = kMaxSms, heads = 8 * nt;
     Workspace w{};
@@ -1055,8 +1089,8 @@ Workspace workspace_of(int H, int Hkv, int d, int bits) {
 using namespace fa;
 
 extern "C" size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits) {
-    if (kvq_check_pool(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
-    return workspace_of(H, Hkv, d, bits).total;
+    if (check_sizes(B, H, Hkv, 1, page_size, max_blocks, d, bits) != FA_OK) return 0;
+    return workspace_of(H, Hkv, d).total;
 }
 
 extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const void* vpages, const int* block_table,
@@ -1064,7 +1098,7 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
                                      int page_size, int max_blocks, int d, int bits, float scale, int o_dtype,
                                      void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !kpages || !vpages || !block_table || !kv_lens || !o || !lse) return FA_ERR_INVALID_ARG;
-    int rc = kvq_check_pool(B, H, Hkv, num_pages, page_size, max_blocks, d, bits);
+    int rc = check_sizes(B, H, Hkv, num_pages, page_size, max_blocks, d, bits);
     if (rc != FA_OK) return rc;
     if (o_dtype != FA_DT_BF16 && o_dtype != FA_DT_F32) return FA_ERR_UNSUPPORTED;
     if (!scale_ok(scale)) return FA_ERR_INVALID_ARG;
@@ -1073,11 +1107,9 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
         return FA_ERR_INVALID_ARG;
     const int nt = tiles_of(H / Hkv, d);
     DecodeQuantParams p{};
-    p.sets = (H / Hkv + 8 * nt - 1) / (8 * nt);
+    p.sets = sets_of(H / Hkv, nt);
     p.cap = max_blocks * page_size;
-    // units are counted in int32, a little past the last one too; 16 keys is the shortest, with 6 more a set
-    if (static_cast<long long>(B) * Hkv * p.sets * ((p.cap - 1LL) / 16 + 7) > 0x7FFFFF00LL) return FA_ERR_INVALID_ARG;
-    const Workspace at = workspace_of(H, Hkv, d, bits);
+    const Workspace at = workspace_of(H, Hkv, d);
     if (!workspace || !kvq_aligned(workspace, 256) || workspace_bytes < at.total) return FA_ERR_WORKSPACE;
     if ((rc = prepare_device(&p.status)) != FA_OK) return rc;
     int dev = 0, num_sms = 0;
@@ -1106,11 +1138,6 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o_dtype = o_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (d == 256) e = bits == 4 ? launch<256, 4, 1>(p, dev, num_sms, s) : launch<256, 8, 1>(p, dev, num_sms, s);
-    else if (d == 128 && nt == 1) e = bits == 4 ? launch<128, 4, 1>(p, dev, num_sms, s) : launch<128, 8, 1>(p, dev, num_sms, s);
-    else if (d == 128) e = bits == 4 ? launch<128, 4, 2>(p, dev, num_sms, s) : launch<128, 8, 2>(p, dev, num_sms, s);
-    else if (nt == 1) e = bits == 4 ? launch<64, 4, 1>(p, dev, num_sms, s) : launch<64, 8, 1>(p, dev, num_sms, s);
-    else e = bits == 4 ? launch<64, 4, 2>(p, dev, num_sms, s) : launch<64, 8, 2>(p, dev, num_sms, s);
+    const cudaError_t e = by_kernel(d, bits, nt, [&](auto D, auto BITS, auto NT) { return launch<D(), BITS(), NT()>(p, dev, num_sms, s); });
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -297,7 +297,12 @@ int fa_kvcache_read_quant(const void* kpages, const void* vpages, const int* cu_
                           const int* kv_lens, void* k_out, void* v_out, int B, int H, int Hkv, int total, int max_seqlen,
                           int num_pages, int page_size, int max_blocks, int d, int bits, int o_dtype, void* stream);
 
-/* Workspace bytes fa_decode_paged_quant needs (256-byte aligned, not initialised); 0 for invalid arguments. */
+/*
+ * Workspace bytes fa_decode_paged_quant needs (256-byte aligned, not initialised); 0 for invalid arguments, and
+ * where the batch at its capacity, max_blocks * page_size keys a sequence, is more than one call counts (then it
+ * returns FA_ERR_INVALID_ARG).  One with B * Hkv * ceil(H / Hkv / 8) * (max_blocks * page_size / 16 + 5) <= 2^31 - 256
+ * is always taken.
+ */
 size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_blocks, int page_size, int d, int bits);
 
 /*
