@@ -94,7 +94,7 @@ struct DecodeQuantParams {
     int4* cut;        // [CTAs]: the set that is cut at a CTA's first unit: (first row of o, heads, first CTA of it, CTAs); 0 CTAs if none is
     int* used;        // CTAs that have units
     int B, H, Hkv, num_pages, page_shift, max_blocks, cap, sets;  // sets: head sets of a KV head
-    float scale, scale_log2;
+    float scale_log2;
     int o_dtype;
 };
 
@@ -1134,7 +1134,6 @@ extern "C" int fa_decode_paged_quant(const void* q, const void* kpages, const vo
     p.num_pages = num_pages;
     p.page_shift = kvq_page_shift(page_size);
     p.max_blocks = max_blocks;
-    p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o_dtype = o_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
