@@ -58,6 +58,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -78,7 +79,7 @@ __host__ __device__ constexpr int warps_of(int d, int bits, int nt) {
 }
 constexpr float kRefBits = 6.0f;    // u is 2^kRefBits at the running maximum
 constexpr float kGrowBits = 8.0f;   // ... and the maximum may be passed by this before a rescale
-constexpr float kNoMax = -1e30f;    // the maximum of no score: finite, so that no difference is NaN
+constexpr float kNoMax = -FLT_MAX;  // the maximum of no score: below any, and finite, so that no difference is NaN
 
 struct DecodeQuantParams {
     const __nv_bfloat16* q;  // [B, H, D]

@@ -116,3 +116,37 @@ def test_decode_outputs_of_long_sequences(cuda_device, lens, H, Hkv, ps, d, bits
 @pytest.mark.parametrize("d,bits,H,Hkv", [(64, 8, 1, 1), (64, 8, 9, 1), (128, 8, 12, 1)])
 def test_decode_average_of_many_values_in_the_other_formats(cuda_device, d, bits, H, Hkv):
     kvq.test_decode_average_of_many_values(cuda_device, d, bits, H, Hkv)
+
+
+def constant_keys(lo, ps, d, bits):
+    """Pool of keys that are lo [keys, d / 32] in all dimensions of a group, exactly; page i holds keys ps i and on."""
+    n = lo.shape[0]
+    pool = np.zeros((-(-n // ps), 1, ps // 16, 16 * ref.row_bytes(d, bits)), np.uint8)
+    par = np.zeros((pool.shape[0] * ps, d // 32, 2), np.uint32)
+    par[:n, :, 0] = lo.astype(np.float32).view(np.uint32) >> 16
+    pool[..., 16 * d * bits // 8:] = par.astype(np.uint16).view(np.uint8).reshape(*pool.shape[:3], -1)
+    return pool.reshape(pool.shape[0], 1, -1)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_scores_far_from_zero(cuda_device, d, bits):
+    """Equal scores of -2^105 and 2^105.  lse is the score, and a single key's output its value (within 2^-11 of its terms:
+    the value, its offset and its range, 8 at most in these pools).  More keys are averaged by each warp, but their parts merged
+    by log-sum-exps that end at 2^82, where log2 of a part's number of keys is lost: parts of any size count the same, and the
+    outputs lie among the values, as weights that are not negative and sum to 1 have it."""
+    dev, ps, lens = cuda_device, 16, [1, 40, 700]
+    table, pages = kvq.make_table(lens, ps, 0, seed=1)
+    kpool = constant_keys(np.full((pages * ps, d // 32), 2.0 ** 45), ps, d, bits)
+    vpool = ref.random_pool(pages, 1, ps, d, bits, seed=170)
+    q = torch.full((3, 2, d), 2.0 ** 60, dtype=torch.bfloat16)
+    q[:, 0] = -q[:, 0]
+    o, lse = fa.decode_paged_quant(q.to(dev), torch.from_numpy(kpool).to(dev), torch.from_numpy(vpool).to(dev),
+                                   kvq.i32(table, dev), kvq.i32(lens, dev), bits, scale=1.0 / d)
+    assert fa.fa_check_status() == fa.FA_OK
+    for b, n in enumerate(lens):
+        v = ref.values(vpool, table[b], range(n), d, bits, ref.V_UNIT)[:, 0]
+        tol = 3 * 2.0 ** -11 * 8
+        assert ((to_np(o)[b] >= v.min(0) - tol) & (to_np(o)[b] <= v.max(0) + tol)).all()
+    off = np.abs(to_np(lse) / 2.0 ** 105 - [-1, 1])
+    assert off.max() <= 2.0 ** -20
