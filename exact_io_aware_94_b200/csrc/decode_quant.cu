@@ -665,7 +665,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
                 for (int i = 1; i < 4 * NB; ++i) mx[nt] = fmaxf(mx[nt], u[nt][i]);
                 mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 1));
                 mx[nt] = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 2));
-                grow |= mx[nt] > m[nt] + kGrowBits;
+                grow |= mx[nt] + (kRefBits - m[nt]) > kRefBits + kGrowBits;  // u's exponent, rounded as below
             }
             if (__any_sync(0xffffffffu, grow)) {
                 uint32_t top = 0;  // greatest magnitude of the group's s 2^kSUp and offsets in the unit, as fp32 bits; NaN left out

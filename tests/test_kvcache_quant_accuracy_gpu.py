@@ -150,3 +150,35 @@ def test_decode_scores_far_from_zero(cuda_device, d, bits):
         assert ((to_np(o)[b] >= v.min(0) - tol) & (to_np(o)[b] <= v.max(0) + tol)).all()
     off = np.abs(to_np(lse) / 2.0 ** 105 - [-1, 1])
     assert off.max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("d,bits,warps", [(64, 4, 12), (64, 8, 16), (128, 4, 12), (128, 8, 12), (256, 4, 8), (256, 8, 8)])
+def test_decode_large_scores_that_rise_by_8_bits(cuda_device, d, bits, warps):
+    """Scores of 1.5 2^26 in base 2, where fp32 ends at 8, that rise by 8 half-way through each sequence.  They are exact, so the
+    output is the average of the values with weights of 2^-8 and 1, but for three roundings of 2^-11 as above.  A sequence that
+    is cut between warps is merged by log-sum-exps that end at 8 too, which may move weight from one part to the other: with
+    as many sequences as warps those are the fewest, and their outputs still lie among the values."""
+    dev, ps, n, rise = cuda_device, 64, 320, 160
+    B = torch.cuda.get_device_properties(dev).multi_processor_count * warps
+    lo = np.zeros((n, d // 32))
+    lo[:, 0] = 1.5 * 2.0 ** 14
+    lo[rise:, 1] = 8.0
+    kpool = constant_keys(lo, ps, d, bits)
+    vpool = ref.random_pool(n // ps, 1, ps, d, bits, seed=171)
+    q = torch.zeros(B, 1, d, dtype=torch.bfloat16)
+    q[:, :, 0], q[:, :, 32] = 2.0 ** 12, 1.0
+    scale = float(np.float32(1.0) / np.float32(1.4426950408889634))
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 1.0
+    table = torch.arange(n // ps, dtype=torch.int32, device=dev).repeat(B, 1)
+    lens = torch.full((B,), n, dtype=torch.int32, device=dev)
+    o, _ = fa.decode_paged_quant(q.to(dev), torch.from_numpy(kpool).to(dev), torch.from_numpy(vpool).to(dev), table, lens,
+                                 bits, scale=scale)
+    assert fa.fa_check_status() == fa.FA_OK
+    v = ref.values(vpool, np.arange(n // ps), range(n), d, bits, ref.V_UNIT)[:, 0]
+    w = np.where(np.arange(n) < rise, 2.0 ** -8, 1.0)
+    tol = 3 * 2.0 ** -11 * 8
+    o = to_np(o)[:, 0]
+    assert np.isfinite(o).all()
+    assert ((o >= v.min(0) - tol) & (o <= v.max(0) + tol)).all()
+    exact = np.abs(o - w @ v / w.sum()).max(-1) <= tol
+    assert exact.mean() >= 0.5
