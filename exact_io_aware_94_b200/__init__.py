@@ -525,7 +525,8 @@ def kvcache_read_quant(kpages, vpages, cu_seqlens, block_table, kv_lens, total, 
 def decode_paged_quant(q, kpages, vpages, block_table, kv_lens, bits, scale=None, out_dtype=torch.float32, ws=None,
                        stream=None):
     """decode_paged over a quantised cache: o [B,H,d] and lse [B,H] for q [B,H,d] (bf16), pools
-    [num_pages,Hkv,page bytes] (uint8), block_table int32 [B,max_blocks] and kv_lens int32 [B] (device)."""
+    [num_pages,Hkv,page bytes] (uint8), block_table int32 [B,max_blocks] and kv_lens int32 [B] (device).  The values' weights
+    are rounded to fp16, 11 bits: o is about that exact, beside the values it averages, in float32 too; lse is an fp32 sum."""
     dev = _kvq_device(q, "q")
     if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bfloat16 tensor [B, H, d]")

@@ -44,8 +44,8 @@
 // ahead of its own (batches with short sequences: 5 % of the time; 48 and 96 keys are within 2 % of it).  The units
 // of the whole batch, in that order, are cut into equal runs, one a CTA, and a CTA's run
 // into equal runs for its warps.  There is one CTA an SM: its warps advance together.
-// (Of three smaller CTAs on an SM the one that came first ran ahead, and the last one was left alone at the end: 203,
-// 230 and 264 us for the same work at 64 x 32,768 keys; one CTA ends at 244.)  A warp copies its units into a ring of S
+// (Of three smaller CTAs on an SM the one that came first ran ahead, and the last one was left alone at the end: 64 x
+// 32,768 keys, calls in a row at the power limit, 1.72 GHz, took 311 us against 298.)  A warp copies its units into a ring of S
 // stages of its own with 16-byte asynchronous copies (a 16-token tile of K or of V is
 // one run of bytes) and waits for no other warp: a set that lies in its run whole it
 // writes out itself.  A set that is cut at a warp's border leaves a part (normalised output and log-sum-exp) on
@@ -72,8 +72,8 @@ namespace {
 
 constexpr int kMaxSms = 160;  // CTAs of a launch, one an SM; bounds the workspace
 // Warps of a CTA: 16, 12 or 8 leave a thread 128, 168 or 255 registers, of which O alone
-// takes nt d / 4.  (Four more with q in shared memory were no faster: 281 -> 289 us at d = 128, 48 -> 51 us at
-// d = 256.)  At d = 64 in 4 bits, 12 leave the shared memory for units of 64 keys.
+// takes nt d / 4.  (Four more with q in shared memory were no faster, the two in turn when a call took more for other
+// reasons: 281 -> 289 us for 64 x 32,768 keys at d = 128, 48 -> 51 us for 5 x 65,536 at d = 256.)  At d = 64 in 4 bits, 12 leave the shared memory for units of 64 keys.
 __host__ __device__ constexpr int warps_of(int d, int bits, int nt) {
     return nt * d <= 64 && bits == 8 ? 16 : nt * d <= 128 ? 12 : 8;
 }
@@ -897,7 +897,9 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
 
 // CTA i - 1 of the grid: the set that is cut at CTA i's first unit.  A set cut over P
 // CTAs has P - 1 such blocks, each of which merges a share of its outputs, four at a time.  What bounds it
-// is the latency of its loads, so all that a thread needs is asked for at once: 6 us with the loads in turn, 2 us so.
+// is latency, so all that a thread needs is asked for at once.  Of the 3 us from the split kernel's last CTA to its own end
+// (96 x 4,001 keys at d = 64, calls in a row) 1.7 pass before its first block runs; by itself and with cold caches, as a
+// profiler runs it, it takes 6.
 constexpr int kCombineThreads = 256;
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
@@ -907,7 +909,7 @@ __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x + 1;
     // (No launch_dependents here: blocks of the next call's split kernel would be dealt out while this kernel's hold
-    // places, unevenly: 28 -> 34 us at 96 x 4,001 keys, 57 -> 71 us at 16 x 8,192.)
+    // places, unevenly: calls in a row, 28 -> 34 us at 96 x 4,001 keys, 57 -> 71 us at 16 x 8,192.)
     kvq_wait_for_previous();
     const int status = *static_cast<volatile const int*>(p.status);
     const int used = *p.used;

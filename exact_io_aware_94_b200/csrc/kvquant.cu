@@ -126,8 +126,8 @@ __device__ __forceinline__ void kvq_quantise(const uint32_t (&w)[8], uint32_t (&
     constexpr float y = 1.0f / kMax;
     const float d = __fsub_rn(hi, lo), q = __fmul_rn(d, y);
     float s = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-kMax, q, d), y, q)));
-    // 1 / s rounded to nearest: the approximation is within 2^-22, the step squares that, and 1 / s of an 8-bit s
-    // is a power of two or at least 2^-34 of itself away from where the rounding turns
+    // 1 / s rounded to nearest, by a step of Newton's method: the approximation is within 2^-22, the step squares that, and
+    // 1 / s of an 8-bit s is a power of two or at least 2^-34 of itself away from where the rounding turns
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     float inv = fmaf(fmaf(-s, r, 1.0f), r, r);

@@ -65,8 +65,8 @@ inline int kvq_page_shift(int page_size) {
     return shift;
 }
 // Launches a kernel whose blocks may be set up while the stream's previous kernel ends; it has to call
-// kvq_wait_for_previous before it touches memory.  Calls one after the other are 1 to 2.5 us closer so (96 x 4,001 keys
-// at d = 64: 30.0 -> 28.0 us, 5 x 65,536 at d = 256: 41.0 -> 38.4 us).
+// kvq_wait_for_previous before it touches memory.  Calls in a row are 1 to 2.5 us closer so (decode when this came: 96 x
+// 4,001 keys at d = 64 30.0 -> 28.0 us, 5 x 65,536 at d = 256 41.0 -> 38.4 us).
 template <typename... P, typename... A>
 inline cudaError_t kvq_launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
     cudaLaunchAttribute early{};

@@ -273,8 +273,8 @@ size_t fa_kvcache_quant_page_bytes(int page_size, int d, int bits);
  * rows than max_seqlen_new or than kv_lens[b] is skipped and flagged
  * FA_ERR_SEQLEN; one whose length is outside [0, max_blocks * page_size] is
  * skipped and flagged FA_ERR_KV_LEN; a row whose page is outside [0, num_pages)
- * is not written and flagged FA_ERR_PAGE.  total_new = 0 returns FA_OK without a
- * launch.
+ * is not written and flagged FA_ERR_PAGE.  total_new = 0 or max_seqlen_new = 0
+ * returns FA_OK without a launch (nothing is written or flagged).
  */
 int fa_kvcache_append_quant(const void* k, const void* v, long long stride_k, long long stride_v, void* kpages,
                             void* vpages, const int* cu_seqlens_new, const int* block_table, const int* kv_lens, int B,
@@ -291,7 +291,8 @@ int fa_kvcache_append_quant(const void* k, const void* v, long long stride_k, lo
  * o_dtype.  Invalid sequences are skipped and flagged as by
  * fa_kvcache_append_quant (their rows are not written); a page outside
  * [0, num_pages) is flagged FA_ERR_PAGE and read as page 0.  Rows at or past
- * cu_seqlens[B] are not written.
+ * cu_seqlens[B] are not written.  total = 0 or max_seqlen = 0 returns FA_OK
+ * without a launch (nothing is written or flagged).
  */
 int fa_kvcache_read_quant(const void* kpages, const void* vpages, const int* cu_seqlens, const int* block_table,
                           const int* kv_lens, void* k_out, void* v_out, int B, int H, int Hkv, int total, int max_seqlen,
@@ -311,9 +312,10 @@ size_t fa_decode_paged_quant_workspace_size(int B, int H, int Hkv, int max_block
  * o [B, H, d] (o_dtype), lse [B, H] fp32, and the device-side conditions
  * (FA_ERR_KV_LEN, FA_ERR_PAGE, a length of 0) are those of fa_decode_paged.
  * What a page holds past a sequence's length never changes a result.
- * The weights of the values are rounded to fp16 (2^-11 of each term).  A value's
- * own error is at most 2^-22 of the largest magnitude that its group of
- * FA_KVQ_GROUP dimensions takes in the sequence's V, whatever the weights: values
+ * The weights of the values, their offsets and their weighted steps are rounded to
+ * fp16 (2^-11 of each term), so fp32 outputs are not exact to fp32's digits.  What a
+ * value loses beside that is at most 2^-22 of the largest magnitude that its group of
+ * FA_KVQ_GROUP dimensions takes in the sequence's V (or 2^-123), whatever the weights: values
  * 2^13 times smaller than another token's in the same group are held to 2^-9 of
  * themselves, those 2^22 times smaller are lost beside it.
  */
