@@ -899,7 +899,7 @@ __global__ void __launch_bounds__((Cfg<D, BITS, NT>::kThreads), 1) fa_decode_qua
 // CTAs has P - 1 such blocks, each of which merges a share of its outputs, four at a time.  What bounds it
 // is latency, so all that a thread needs is asked for at once.  Of the 3 us from the split kernel's last CTA to its own end
 // (96 x 4,001 keys at d = 64, calls in a row) 1.7 pass before its first block runs; by itself and with cold caches, as a
-// profiler runs it, it takes 6.
+// profiler runs it, it takes 5 to 6.
 constexpr int kCombineThreads = 256;
 template <int D, int BITS, int NT>
 __global__ void __launch_bounds__(kCombineThreads) fa_decode_quant_combine(const __grid_constant__ DecodeQuantParams p) {
