@@ -182,3 +182,21 @@ def test_decode_large_scores_that_rise_by_8_bits(cuda_device, d, bits, warps):
     assert ((o >= v.min(0) - tol) & (o <= v.max(0) + tol)).all()
     exact = np.abs(o - w @ v / w.sum()).max(-1) <= tol
     assert exact.mean() >= 0.5
+
+
+@pytest.mark.parametrize("log2_spread", [-90, -105, -115])
+@pytest.mark.parametrize("d,bits", [(64, 8), (128, 4)])
+def test_decode_tiny_values(cuda_device, d, bits, log2_spread):
+    """Values near fp32's least: below 2^-100 a group's power of two stays 2^-100, so an offset is off by 2^-125 and a step's
+    part by twice that, 2^-123 with the products' roundings (2^-31 2^-100 2 of the greatest weight, of 200 keys)."""
+    dev, ps, lens = cuda_device, 16, [200, 37]
+    table, pages = kvq.make_table(lens, ps, 1, seed=5)
+    kpool = ref.random_pool(pages, 1, ps, d, bits, seed=180)
+    vpool = ref.random_pool(pages, 1, ps, d, bits, seed=181, spread=2.0 ** log2_spread)
+    q = torch.randn(2, 3, d, generator=torch.Generator().manual_seed(182)).to(torch.bfloat16)
+    o_ref, tol = decode64(q.double().numpy(), kpool, vpool, table, lens, bits, 0.1)
+    o, _ = fa.decode_paged_quant(q.to(dev), torch.from_numpy(kpool).to(dev), torch.from_numpy(vpool).to(dev),
+                                 kvq.i32(table, dev), kvq.i32(lens, dev), bits, scale=0.1)
+    assert fa.fa_check_status() == fa.FA_OK
+    over = np.abs(to_np(o) - o_ref) / (tol + 2.0 ** -123)
+    assert over.max() <= 1.0, "o beyond its tolerance by a factor of %.3g" % over.max()
